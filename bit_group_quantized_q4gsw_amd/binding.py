@@ -62,6 +62,20 @@ class AdamwParams(ctypes.Structure):
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float)]
 
 
+class KvCacheDesc(ctypes.Structure):
+    """q4gsw_kv_cache of include/q4gsw.h."""
+    _fields_ = [("pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("reserved", ctypes.c_int32), ("data", ctypes.c_void_p),
+                ("bytes", ctypes.c_uint64)]
+
+
+class KvSeqs(ctypes.Structure):
+    """q4gsw_kv_seqs of include/q4gsw.h."""
+    _fields_ = [("table", ctypes.c_void_p), ("table_ld", ctypes.c_int64), ("table_cols", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("cu", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("tokens", ctypes.c_int64)]
+
+
 # Choices made by forced_route / forced_plan, held per Python thread and handed to each call
 # (the library itself keeps no routing state).
 _local = threading.local()
@@ -89,6 +103,7 @@ def lib() -> ctypes.CDLL:
         i32, i64, u64, vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
         pw = ctypes.POINTER(WeightDesc)
         po = ctypes.POINTER(Options)
+        pc, ps = ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvSeqs)
         sigs = {
             "q4gsw_packed_bytes": [i64, i64, i64, i32, ctypes.POINTER(u64)],
             "q4gsw_pack": [vp, vp, i32, i64, i64, i64, vp, u64, vp, pw],
@@ -110,6 +125,15 @@ def lib() -> ctypes.CDLL:
             "q4gsw_dq8ca_quantize": [vp, i32, i64, i64, vp, vp, vp, vp],
             "q4gsw_linear_dq8ca": [pw, vp, i32, i64, vp, vp, u64, vp],
             "q4gsw_linear_dq8ca_ex": [pw, vp, i32, i64, vp, vp, u64, po, vp],
+            "q4gsw_dq8ca_rows_bytes": [i64, i64, ctypes.POINTER(u64)],
+            "q4gsw_rmsnorm_dq8ca": [vp, i32, vp, vp, i32, i64, i64, ctypes.c_float, vp, vp, u64, vp, vp],
+            "q4gsw_dq8ca_rows_workspace_bytes": [pw, i64, ctypes.POINTER(u64)],
+            "q4gsw_linear_dq8ca_rows": [pw, vp, u64, i64, vp, vp, u64, vp],
+            "q4gsw_kv_bytes": [pc, ctypes.POINTER(u64)],
+            "q4gsw_kv_append": [pc, ps, vp, i64, vp, i64, i32, vp],
+            "q4gsw_kv_read": [pc, ps, vp, vp, vp],
+            "q4gsw_kv_attention_workspace_bytes": [pc, i32, i64, i32, i32, i32, ctypes.POINTER(u64)],
+            "q4gsw_kv_attention": [pc, ps, vp, i64, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, u64, vp],
             "q4gsw_adapter_workspace_bytes": [i32, pw, i64, i32, i32, ctypes.POINTER(u64)],
             "q4gsw_adapter_fwd": [pw, vp, i32, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, u64, vp],
             "q4gsw_adapter_bwd": [pw, vp, vp, i32, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, vp, vp, u64, vp],
@@ -324,6 +348,182 @@ def linear_dq8ca(w: PackedWeight, x: torch.Tensor, out: Optional[torch.Tensor] =
     _check(lib().q4gsw_linear_dq8ca_ex(w.ref(), x.data_ptr(), _TORCH_DTYPE[x.dtype], M, y.data_ptr(), wp, wb,
                                        _opts(), _stream()), "q4gsw_linear_dq8ca")
     return y
+
+
+class Dq8caRows:
+    """M rows of K int8 activations in the int8 linear's layout, written by rmsnorm_dq8ca and read
+    by linear_dq8ca_rows: codes, row scales and zero points in one device buffer."""
+
+    def __init__(self, M: int, K: int, buffer: torch.Tensor):
+        self.M = M
+        self.K = K
+        self.buffer = buffer
+
+
+def dq8ca_rows(M: int, K: int, device="cuda") -> Dq8caRows:
+    """An (unwritten) rows buffer for M rows of K columns."""
+    out = ctypes.c_uint64()
+    _check(lib().q4gsw_dq8ca_rows_bytes(M, K, ctypes.byref(out)), "q4gsw_dq8ca_rows_bytes")
+    return Dq8caRows(M, K, torch.empty(out.value, dtype=torch.uint8, device=device))
+
+
+def rmsnorm_dq8ca(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                  rows: Optional[Dq8caRows] = None, h: Optional[torch.Tensor] = None,
+                  values: Optional[torch.Tensor] = None):
+    """(rows, h, values): h = round(x + residual) in weight's dtype (x itself rounded, without a
+    residual), rows = h * weight / sqrt(mean(h^2) + eps) in int8 codes with a scale and a zero point
+    per row, for linear_dq8ca_rows.  `h` may be `residual` itself (updated in place); without a
+    residual it is written only if given.  `values` (fp32 [M, K]) receives what the rows stand for
+    if given."""
+    x = _dev(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    if not weight.is_cuda or tuple(weight.shape) != (K,) or weight.device != x.device or weight.dtype not in _TORCH_DTYPE:
+        raise ValueError(f"weight must be a floating tensor of shape [{K}] on {x.device}")
+    weight = weight.contiguous()
+    dt = weight.dtype
+    if residual is not None:
+        if residual.dtype != dt or residual.shape != x.shape or residual.device != x.device:
+            raise ValueError(f"residual must be {dt} [M, K] on {x.device}")
+        residual = residual.contiguous()
+        if h is None:
+            h = torch.empty_like(residual)
+    if h is not None and (h.dtype != dt or h.shape != x.shape or h.device != x.device or not h.is_contiguous()):
+        raise ValueError(f"h must be a contiguous {dt} tensor [M, K] on {x.device}")
+    if rows is None:
+        rows = dq8ca_rows(M, K, x.device)
+    elif rows.M != M or rows.K != K or rows.buffer.device != x.device:
+        raise ValueError(f"rows must hold [{M}, {K}] on {x.device}")
+    if values is not None:
+        _out(values, (M, K), x.device, "values")
+    _check(lib().q4gsw_rmsnorm_dq8ca(
+        x.data_ptr(), _TORCH_DTYPE[x.dtype], residual.data_ptr() if residual is not None else None, weight.data_ptr(),
+        _TORCH_DTYPE[dt], M, K, eps, h.data_ptr() if h is not None else None, rows.buffer.data_ptr(),
+        rows.buffer.numel(), values.data_ptr() if values is not None else None, _stream()), "q4gsw_rmsnorm_dq8ca")
+    return rows, h, values
+
+
+def linear_dq8ca_rows(w: PackedWeight, rows: Dq8caRows, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [M, N] fp32 = linear_dq8ca of rows that are quantised already."""
+    if rows.K != w.K:
+        raise ValueError("rows must have w.K columns")
+    dev = rows.buffer.device
+    y = _out(out, (rows.M, w.N), dev, "out")
+    need = ctypes.c_uint64()
+    _check(lib().q4gsw_dq8ca_rows_workspace_bytes(w.ref(), rows.M, ctypes.byref(need)), "q4gsw_dq8ca_rows_workspace_bytes")
+    ws, wp, wb = _ws_args(need.value, workspace, dev)
+    _check(lib().q4gsw_linear_dq8ca_rows(w.ref(), rows.buffer.data_ptr(), rows.buffer.numel(), rows.M, y.data_ptr(), wp,
+                                         wb, _stream()), "q4gsw_linear_dq8ca_rows")
+    return y
+
+
+class KvCache:
+    """A paged cache of keys and values in 4 bits: the descriptor and its device buffer."""
+
+    def __init__(self, desc: KvCacheDesc, buffer: torch.Tensor):
+        self.desc = desc
+        self.buffer = buffer
+        self.pages, self.page_size, self.heads, self.dim = desc.pages, desc.page_size, desc.heads, desc.dim
+        self._ref = ctypes.byref(desc)
+
+
+def kv_cache(pages: int, page_size: int, heads: int, dim: int, device="cuda") -> KvCache:
+    """An empty cache (zeros) of `pages` pages of page_size tokens."""
+    desc = KvCacheDesc(pages, page_size, heads, dim, 0, None, 0)
+    out = ctypes.c_uint64()
+    _check(lib().q4gsw_kv_bytes(ctypes.byref(desc), ctypes.byref(out)), "q4gsw_kv_bytes")
+    buf = torch.zeros(out.value, dtype=torch.uint8, device=device)
+    desc.data, desc.bytes = buf.data_ptr(), out.value
+    return KvCache(desc, buf)
+
+
+def _kv_seqs(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, tokens: int) -> KvSeqs:
+    dev = cache.buffer.device
+    B = lens.shape[0] if lens.dim() == 1 else -1
+    if lens.dtype != torch.int32 or B < 1 or lens.device != dev or not lens.is_contiguous():
+        raise ValueError(f"lens must be a contiguous int32 tensor [batch] on {dev}")
+    if cu.dtype != torch.int32 or tuple(cu.shape) != (B + 1,) or cu.device != dev or not cu.is_contiguous():
+        raise ValueError(f"cu must be a contiguous int32 tensor [batch + 1] on {dev}")
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B or table.device != dev \
+            or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be an int32 tensor [batch, pages per sequence] with dense rows on {dev}")
+    cols = table.shape[1]
+    ld = table.stride(0) if B > 1 else cols
+    if ld < cols:
+        raise ValueError("table's rows must not overlap")
+    return KvSeqs(table.data_ptr(), ld, cols, B, cu.data_ptr(), lens.data_ptr(), tokens)
+
+
+def _token_rows(t: torch.Tensor, heads: int, dim: int, device, name: str) -> Tuple[torch.Tensor, int]:
+    """(tensor, token pitch in elements): `t` itself where its token rows are dense and 16-byte
+    aligned (a slice of a fused projection's output, say), else a copy."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.device != device or t.dtype not in _TORCH_DTYPE:
+        raise ValueError(f"{name} must be a floating tensor [tokens, {heads}, {dim}] on {device}")
+    ld = t.stride(0) if t.shape[0] > 1 else heads * dim
+    es = t.element_size()
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim) or ld < heads * dim or (ld * es) % 16 or t.data_ptr() % 16:
+        t = t.clone(memory_format=torch.contiguous_format)
+        ld = heads * dim
+    return t, ld
+
+
+def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, cu: torch.Tensor,
+              lens: torch.Tensor) -> None:
+    """Store the keys and values k, v [tokens, heads, dim] of new tokens: rows cu[b] .. cu[b + 1] - 1
+    are the last of sequence b's lens[b] tokens (with them), whose pages are table[b]."""
+    dev = cache.buffer.device
+    k, k_ld = _token_rows(k, cache.heads, cache.dim, dev, "k")
+    v, v_ld = _token_rows(v, cache.heads, cache.dim, dev, "v")
+    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have one dtype and one number of tokens")
+    seqs = _kv_seqs(cache, table, cu, lens, k.shape[0])
+    _check(lib().q4gsw_kv_append(cache._ref, ctypes.byref(seqs), k.data_ptr(), k_ld, v.data_ptr(), v_ld,
+                                 _TORCH_DTYPE[k.dtype], _stream()), "q4gsw_kv_append")
+
+
+def kv_read(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, tokens: int,
+            out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(k, v) fp32 [tokens, heads, dim]: what the cache stands for at the places kv_append with the
+    same table, cu and lens writes."""
+    dev = cache.buffer.device
+    shape = (tokens, cache.heads, cache.dim)
+    k, v = (_out(o, shape, dev, name) for o, name in zip(out if out is not None else (None, None), ("k", "v")))
+    seqs = _kv_seqs(cache, table, cu, lens, tokens)
+    _check(lib().q4gsw_kv_read(cache._ref, ctypes.byref(seqs), k.data_ptr(), v.data_ptr(), _stream()), "q4gsw_kv_read")
+    return k, v
+
+
+def kv_attention_workspace_bytes(cache: KvCache, batch: int, tokens: int, hq: int, max_new: int, max_ctx: int) -> int:
+    """Workspace of kv_attention calls with these sizes (any window)."""
+    out = ctypes.c_uint64()
+    _check(lib().q4gsw_kv_attention_workspace_bytes(cache._ref, batch, tokens, hq, max_new, max_ctx, ctypes.byref(out)),
+           "q4gsw_kv_attention_workspace_bytes")
+    return out.value
+
+
+def kv_attention(cache: KvCache, q: torch.Tensor, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor,
+                 max_new: int, max_ctx: int, window: int = 0, softcap: float = 0.0,
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out [tokens, hq, dim] of q's dtype: causal attention of the new tokens q over the cache, which
+    holds their own keys and values already.  max_new and max_ctx bound the sequences' new tokens and
+    lengths; window > 0 keeps the last `window` keys of each token, softcap > 0 caps the scores."""
+    dev = cache.buffer.device
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, hq, dim]")
+    tokens, hq = q.shape[0], q.shape[1]
+    q, q_ld = _token_rows(q, hq, cache.dim, dev, "q")
+    if out is None:
+        out = torch.empty(tokens, hq, cache.dim, dtype=q.dtype, device=dev)
+    elif out.dtype != q.dtype or out.shape != q.shape or out.device != dev or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {q.dtype} tensor [tokens, hq, dim] on {dev}")
+    seqs = _kv_seqs(cache, table, cu, lens, tokens)
+    need = kv_attention_workspace_bytes(cache, seqs.batch, tokens, hq, max_new, max_ctx)
+    ws, wp, wb = _ws_args(need, workspace, dev)
+    _check(lib().q4gsw_kv_attention(cache._ref, ctypes.byref(seqs), q.data_ptr(), q_ld, _TORCH_DTYPE[q.dtype], hq, max_new,
+                                    max_ctx, window, softcap, out.data_ptr(), wp, wb, _stream()), "q4gsw_kv_attention")
+    return out
 
 
 def adapter_workspace_bytes(op: int, w: PackedWeight, M: int, dtype: torch.dtype, rank: int) -> int:

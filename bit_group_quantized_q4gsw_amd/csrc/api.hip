@@ -10,15 +10,12 @@
 #include <cstring>
 #include <mutex>
 
-#include "../../include/q4gsw.h"
+#include "api_util.h"
 #include "internal.h"
 
 using namespace q4gsw;
 
 namespace {
-
-constexpr int64_t kMaxDim = int64_t(1) << 30;
-constexpr int64_t kMaxM = int64_t(1) << 23;
 
 // Per-call choices (q4gsw_options), validated: route family, forward block rows, K splits.
 struct Opts {
@@ -38,19 +35,6 @@ q4gsw_status read_opts(const q4gsw_options* o, Opts* out) {
     out->splits = o->splits;
     return Q4GSW_OK;
 }
-
-int esize(int32_t dt) { return dt == Q4GSW_F32 ? 4 : 2; }
-bool act_dtype_ok(int32_t dt) { return dt == Q4GSW_F32 || dt == Q4GSW_F16 || dt == Q4GSW_BF16; }
-bool scale_dtype_ok(int32_t dt) { return dt == Q4GSW_F32 || dt == Q4GSW_F16; }
-
-struct Range {
-    uintptr_t lo, hi;   // [lo, hi)
-};
-Range range_of(const void* p, uint64_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Range{a, a + bytes};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
 
 q4gsw_status check_desc(const q4gsw_weight* w) {
     if (!w) return Q4GSW_E_NULL;
@@ -206,8 +190,6 @@ uint64_t qkv_ws_bytes(const q4gsw_weight* const w[3], int64_t M, int32_t dt, int
     return b;
 }
 
-q4gsw_status hip_status(hipError_t e) { return e == hipSuccess ? Q4GSW_OK : Q4GSW_E_HIP; }
-
 // epi: a low-rank term the MFMA route adds in its reduction or epilogue; *epi_done tells whether
 // this call applied it (the other routes leave it to the caller).
 q4gsw_status run_fwd(const q4gsw_weight* w, const void* x, int32_t dt, int64_t M, float* y, void* ws,
@@ -258,10 +240,6 @@ q4gsw_status run_bwd(const q4gsw_weight* w, const void* d_out, int32_t g_dtype, 
                                               fuse ? epi : nullptr));
         }
     }
-}
-
-bool ws_ok(const void* ws, uint64_t ws_bytes, uint64_t need) {
-    return need == 0 || (ws && ws_bytes >= need && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0);
 }
 
 // Forward validation shared by q4gsw_linear_fwd_ex and the allocation-free forward: descriptor,
@@ -537,6 +515,42 @@ q4gsw_status q4gsw_linear_dq8ca(const q4gsw_weight* w, const void* x, int32_t x_
     return q4gsw_linear_dq8ca_ex(w, x, x_dtype, M, y, ws, ws_bytes, nullptr, stream);
 }
 
+q4gsw_status q4gsw_dq8ca_rows_bytes(int64_t M, int64_t K, uint64_t* bytes) {
+    if (!bytes) return Q4GSW_E_NULL;
+    if (M < 1 || M > kMaxM || K < 1 || K > kMaxDim) return Q4GSW_E_SHAPE;
+    *bytes = dq8ca_rows_total(M, K);
+    return Q4GSW_OK;
+}
+
+q4gsw_status q4gsw_dq8ca_rows_workspace_bytes(const q4gsw_weight* w, int64_t M, uint64_t* bytes) {
+    if (!bytes) return Q4GSW_E_NULL;
+    const q4gsw_status st = check_desc(w);
+    if (st != Q4GSW_OK) return st;
+    if (M < 1 || M > kMaxM) return Q4GSW_E_SHAPE;
+    const WView v = view_of(w);
+    if (!dq8ca_supported(v)) return Q4GSW_E_GROUP;
+    *bytes = (uint64_t)plan_dq8ca(v, M).ws_bytes - dq8ca_rows_total(M, w->K);
+    return Q4GSW_OK;
+}
+
+q4gsw_status q4gsw_linear_dq8ca_rows(const q4gsw_weight* w, const void* rows, uint64_t rows_bytes, int64_t M, float* y,
+                                     void* ws, uint64_t ws_bytes, void* stream) {
+    uint64_t need = 0;
+    q4gsw_status st = q4gsw_dq8ca_rows_workspace_bytes(w, M, &need);
+    if (st != Q4GSW_OK) return st;
+    if (!rows || !y) return Q4GSW_E_NULL;
+    const uint64_t total = dq8ca_rows_total(M, w->K);
+    if (rows_bytes < total) return Q4GSW_E_BUFFER;
+    if (reinterpret_cast<uintptr_t>(rows) & 255u) return Q4GSW_E_ALIGN;
+    if (!ws_ok(ws, ws_bytes, need)) return Q4GSW_E_WORKSPACE;
+    const Range yr = range_of(y, (uint64_t)M * w->N * 4), rr = range_of(rows, total), wr = range_of(w->data, w->bytes);
+    const Range sr = range_of(ws, need);
+    if (overlap(yr, rr) || overlap(yr, wr) || overlap(sr, yr) || overlap(sr, rr) || overlap(sr, wr)) return Q4GSW_E_ALIAS;
+    const WView v = view_of(w);
+    return hip_status(launch_dq8ca_rows(v, dq8ca_rows_at(const_cast<void*>(rows), M, w->K), M, y, plan_dq8ca(v, M), ws,
+                                        static_cast<hipStream_t>(stream)));
+}
+
 q4gsw_status q4gsw_qkv_fused_ex(const q4gsw_weight* wq, const q4gsw_weight* wk, const q4gsw_weight* wv, const void* x,
                                 int32_t x_dtype, int64_t M, float* q, float* k, float* v, void* ws, uint64_t ws_bytes,
                                 const q4gsw_options* opts, void* stream) {
@@ -599,8 +613,6 @@ q4gsw_status q4gsw_qkv_fused(const q4gsw_weight* wq, const q4gsw_weight* wk, con
 }
 
 // ---- the adapter step around the frozen base ----------------------------------------------------
-static bool finite_f(double v) { return v == v && v - v == 0.0; }
-
 q4gsw_status q4gsw_adapter_workspace_bytes(int32_t op, const q4gsw_weight* w, int64_t M, int32_t act_dtype,
                                            int32_t rank, uint64_t* bytes) {
     if (!bytes) return Q4GSW_E_NULL;
@@ -824,6 +836,7 @@ const char* q4gsw_status_str(int32_t status) {
         case Q4GSW_E_BUFFER: return "packed buffer too small";
         case Q4GSW_E_ROUTE: return "requested route cannot serve this call";
         case Q4GSW_E_SCRATCH: return "call needs more than the allocation-free entry point's 32 MiB scratch";
+        case Q4GSW_E_ALIGN: return "pointer or row pitch not a multiple of 16 bytes (rows buffer: 256)";
         default: return "unknown status";
     }
 }

@@ -489,16 +489,37 @@ hipError_t launch_dq8ca_quantize(const void* x, int x_dtype, int64_t M, int64_t 
     return launch_quant<false>(x, x_dtype, M, K, K, q, scale, zp, s);
 }
 
+Dq8caRows dq8ca_rows_at(void* base, int64_t M, int64_t K) {
+    const int64_t kp = round_up(K, kTileCols);
+    uint8_t* p = static_cast<uint8_t*>(base);
+    Dq8caRows r;
+    r.codes = reinterpret_cast<int8_t*>(p);
+    r.scale = reinterpret_cast<float*>(p + dq8ca_codes_bytes(M, kp));
+    r.nzp = reinterpret_cast<int32_t*>(p + dq8ca_codes_bytes(M, kp) + dq8ca_rows_bytes(M));
+    r.ld = kp;
+    return r;
+}
+
+uint64_t dq8ca_rows_total(int64_t M, int64_t K) {
+    return (uint64_t)(dq8ca_codes_bytes(M, round_up(K, kTileCols)) + 2 * dq8ca_rows_bytes(M));
+}
+
 hipError_t launch_dq8ca(const WView& w, const void* x, int x_dtype, int64_t M, float* y, const Dq8caPlan& plan,
                         void* ws, hipStream_t s) {
     if (!dq8ca_supported(w) || M > 0x7fffffff) return hipErrorInvalidValue;
-    uint8_t* base = static_cast<uint8_t*>(ws);
-    int8_t* aq = reinterpret_cast<int8_t*>(base);
-    float* rs = reinterpret_cast<float*>(base + dq8ca_codes_bytes(M, w.k_pad));
-    int32_t* nzp = reinterpret_cast<int32_t*>(base + dq8ca_codes_bytes(M, w.k_pad) + dq8ca_rows_bytes(M));
-    float* part = reinterpret_cast<float*>(base + dq8ca_codes_bytes(M, w.k_pad) + 2 * dq8ca_rows_bytes(M));
-    hipError_t e = launch_quant<true>(x, x_dtype, M, w.K, w.k_pad, aq, rs, nzp, s);
+    const Dq8caRows r = dq8ca_rows_at(ws, M, w.K);
+    const hipError_t e = launch_quant<true>(x, x_dtype, M, w.K, w.k_pad, r.codes, r.scale, r.nzp, s);
     if (e != hipSuccess) return e;
+    return launch_dq8ca_rows(w, r, M, y, plan, static_cast<uint8_t*>(ws) + dq8ca_rows_total(M, w.K), s);
+}
+
+hipError_t launch_dq8ca_rows(const WView& w, const Dq8caRows& rows, int64_t M, float* y, const Dq8caPlan& plan,
+                             void* partials, hipStream_t s) {
+    if (!dq8ca_supported(w) || rows.ld != w.k_pad || M > 0x7fffffff) return hipErrorInvalidValue;
+    const int8_t* aq = rows.codes;
+    const float* rs = rows.scale;
+    const int32_t* nzp = rows.nzp;
+    float* part = static_cast<float*>(partials);
     const int64_t tiles = (w.n_pad + kBN - 1) / kBN;
     const int64_t mtiles = (M + kBM - 1) / kBM;
     const int64_t n_chunks = w.k_pad / kCK;
@@ -518,7 +539,7 @@ hipError_t launch_dq8ca(const WView& w, const void* x, int x_dtype, int64_t M, f
         if (two) hipLaunchKernelGGL((dq8ca_gemm_kernel<0, 2>), grid, dim3(512), 0, s, w, aq, rs, nzp, M, out, ld, stride, per, sp, mt);
         else hipLaunchKernelGGL((dq8ca_gemm_kernel<0, 1>), grid, dim3(512), 0, s, w, aq, rs, nzp, M, out, ld, stride, per, sp, mt);
     }
-    e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || plan.splits == 1) return e;
     const float* ys[1] = {y};
     const int64_t yld[1] = {w.N}, off[1] = {0}, cols[1] = {w.N};

@@ -143,11 +143,38 @@ struct Dq8caPlan {
     int64_t ws_bytes;
 };
 bool dq8ca_supported(const WView& w);
+// Rows quantised for the GEMM: codes [M][ld = k_pad], scales [M], -zero points [M], one after the
+// other in a buffer of dq8ca_rows_total bytes.
+struct Dq8caRows {
+    int8_t* codes;
+    float* scale;
+    int32_t* nzp;
+    int64_t ld;
+};
+uint64_t dq8ca_rows_total(int64_t M, int64_t K);
+Dq8caRows dq8ca_rows_at(void* base, int64_t M, int64_t K);
 Dq8caPlan plan_dq8ca(const WView& w, int64_t M, int force_splits = 0);
 hipError_t launch_dq8ca_quantize(const void* x, int x_dtype, int64_t M, int64_t K, int8_t* q, float* scale,
                                  int32_t* zp, hipStream_t s);
 hipError_t launch_dq8ca(const WView& w, const void* x, int x_dtype, int64_t M, float* y, const Dq8caPlan& plan,
                         void* ws, hipStream_t s);
+// The GEMM alone, on rows already quantised (partials: plan.ws_bytes - dq8ca_rows_total bytes).
+hipError_t launch_dq8ca_rows(const WView& w, const Dq8caRows& rows, int64_t M, float* y, const Dq8caPlan& plan,
+                             void* partials, hipStream_t s);
+
+// norm_dq8ca.hip: h = x + residual (residual, h, values may be null; h, residual and weight in
+// r_dtype), rows = int8 codes of h * weight, the norm's factor in their scales.
+hipError_t launch_rmsnorm_dq8ca(const void* x, int x_dtype, const void* residual, int r_dtype, const void* weight,
+                                int64_t M, int64_t K, float eps, void* h, const Dq8caRows& rows, float* values,
+                                hipStream_t s);
+
+// kv_cache.hip: new tokens' rows (token rows of k_ld / v_ld elements) into the 4-bit cache, and
+// the same places read back as fp32 [tokens][heads][dim].
+struct KvView;
+struct KvSeqs;
+hipError_t launch_kv_append(const KvView& c, const KvSeqs& sq, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                            int dtype, hipStream_t s);
+hipError_t launch_kv_read(const KvView& c, const KvSeqs& sq, float* k, float* v, hipStream_t s);
 
 // adapter.hip: the low-rank adapter terms beside the frozen weight (rank 1..adapter_rank_max())
 // and the AdamW update.  The forward writes t = x A^T [M, r], then y += alpha t B^T; its

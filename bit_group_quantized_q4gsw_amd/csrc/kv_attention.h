@@ -1,0 +1,126 @@
+// Shared by the attention kernels over the 4-bit cache (kv_rows.hip, kv_prompt.hip, kv_join.hip).
+#pragma once
+#include "kv4.h"
+
+namespace q4gsw {
+
+struct KvAttnArgs {
+    KvView c;
+    KvSeqs sq;
+    const void* q;           // token rows of q_ld elements, [hq][dim] dense, of dtype
+    int64_t q_ld;
+    int dtype;
+    void* out;               // [tokens][hq][dim] of dtype (one split)
+    float* part;             // more: [split][tokens][hq][dim] sums, not divided by the weights' sum
+    float* ml;               //       [split][tokens][hq] pairs (reference exponent, weights' sum)
+    int hq, group;           // query heads; of them per head of the cache
+    int max_new;             // rows of later new tokens are not computed
+    int window;              // 0: none
+    float cap_in, cap_out;   // 1 / cap and cap log2(e); 0: no cap
+    float scale;             // dim^-1/2
+    int splits, chunk;       // blocks of 32 tokens per split (the last split takes the rest)
+    int row_tiles;
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNoKey = -3.0e38f;   // reference exponent of a row that has seen no key
+// Weights are 2^(score - reference + kLift): the reference moves only when a score passes it by
+// more than kSlack, so a weight is at most 2^(kLift + kSlack) = 2^14, a finite fp16, and the
+// largest weight of a row is at least 2^kLift, 2^30 times fp16's smallest step.
+constexpr float kLift = 6.0f, kSlack = 8.0f;
+
+// What the rows [r0, r0 + nr) of one (sequence, cache head) see: row r is new token r / group,
+// query head r % group; its place is p0 + r / group.
+struct KvSpan {
+    int pmin, pmax;          // places of the first and last row
+    int64_t lo, hi;          // 32-token blocks [lo, hi) of this split
+};
+__device__ __forceinline__ KvSpan kv_span(const KvAttnArgs& a, const KvSeq& s, int r0, int nr, int split) {
+    KvSpan r;
+    const int p0 = s.len - s.m;
+    r.pmin = p0 + r0 / a.group;
+    r.pmax = p0 + (r0 + nr - 1) / a.group;
+    int64_t first = a.window ? (int64_t)r.pmin - a.window + 1 : 0;
+    first = first < 0 ? 0 : first;
+    int64_t end = r.pmax < 0 ? 0 : (r.pmax >> 5) + 1;
+    const int64_t room = (int64_t)a.sq.table_cols << a.c.bpp_log2;
+    end = end < room ? end : room;
+    r.lo = (first >> 5) + (int64_t)split * a.chunk;
+    r.hi = split == a.splits - 1 ? end : (r.lo + a.chunk < end ? r.lo + a.chunk : end);
+    return r;
+}
+
+// Factor 2^(14 - e), e the exponent of a row's largest magnitude, that brings the row into fp16's
+// range (every bf16 or fp16 value of it down to 2^-19 of the largest stays exact; fp32 values
+// round to 11 bits), and its inverse.  A zero row gets any factor, infinities and NaN stay.
+__device__ __forceinline__ void row_factor(float amax, float& mul, float& inv) {
+    int eb = (int)(bitcast<uint32_t>(amax) >> 23) & 0xFF;
+    eb = eb < 15 ? 15 : eb;
+    mul = bitcast<float>((uint32_t)(268 - eb > 254 ? 254 : 268 - eb) << 23);
+    inv = bitcast<float>((uint32_t)(eb - 14) << 23);
+}
+
+// cap * tanh(x / cap) * log2(e), with in = 1 / cap and out = cap log2(e).  tanh z = 1 - 2 / (1 + e^2z)
+// is off by a few 2^-24 absolute, so below 1/8 its series takes over (next term 2^-24 relative).
+__device__ __forceinline__ float capped_log2(float x, float in, float out) {
+    const float z = x * in;
+    const float big = fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * (2.0f * kLog2e))), 1.0f);
+    const float z2 = z * z;
+    const float small = fmaf(z * z2, fmaf(z2, fmaf(z2, -17.0f / 315.0f, 2.0f / 15.0f), -1.0f / 3.0f), z);
+    return out * (fabsf(z) < 0.125f ? small : big);
+}
+
+// Maximum of v over lanes l, l ^ 16, l ^ 32, l ^ 48, in every lane (NaN counts as nothing).
+__device__ __forceinline__ float wave_max_rows(float v) {
+    const uint32_t a = bitcast<uint32_t>(v);
+    const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    const float s = fmaxf(bitcast<float>(r[0]), bitcast<float>(r[1]));
+    const uint32_t b = bitcast<uint32_t>(s);
+    const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return fmaxf(bitcast<float>(h[0]), bitcast<float>(h[1]));
+}
+
+// Four neighbouring channels of an output row.
+__device__ __forceinline__ void store4(void* out, int dtype, int64_t e, f4 v) {
+    if (dtype == kF32) {
+        *reinterpret_cast<f4*>(static_cast<float*>(out) + e) = v;
+    } else if (dtype == kF16) {
+        const h2 a = {(_Float16)v[0], (_Float16)v[1]}, b = {(_Float16)v[2], (_Float16)v[3]};
+        *reinterpret_cast<u2*>(static_cast<uint16_t*>(out) + e) = u2{bitcast<uint32_t>(a), bitcast<uint32_t>(b)};
+    } else {
+        const b2 a = {(__bf16)v[0], (__bf16)v[1]}, b = {(__bf16)v[2], (__bf16)v[3]};
+        *reinterpret_cast<u2*>(static_cast<uint16_t*>(out) + e) = u2{bitcast<uint32_t>(a), bitcast<uint32_t>(b)};
+    }
+}
+
+// Eight neighbouring channels of a query row (16-byte aligned) as fp32.
+__device__ __forceinline__ void load_q8(const void* q, int dtype, int64_t e, float* v) {
+    if (dtype == kF32) {
+        const f4 a = bitcast<f4>(ldg16(static_cast<const float*>(q) + e));
+        const f4 b = bitcast<f4>(ldg16(static_cast<const float*>(q) + e + 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+        return;
+    }
+    const u4 a = ldg16(static_cast<const uint16_t*>(q) + e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (dtype == kF16) {
+            v[2 * i] = f16_bits_to_f32((uint16_t)(a[i] & 0xFFFFu));
+            v[2 * i + 1] = f16_bits_to_f32((uint16_t)(a[i] >> 16));
+        } else {
+            v[2 * i] = bitcast<float>(a[i] << 16);
+            v[2 * i + 1] = bitcast<float>(a[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+// kv_rows.hip: `waves` (4 or 8) per workgroup, tiles of 16 * r rows (r 2 only up to 128 channels).
+hipError_t launch_kv_rows(const KvAttnArgs& a, int r, int waves, hipStream_t s);
+// The join of the splits' partials into out.
+hipError_t launch_kv_join(const KvAttnArgs& a, hipStream_t s);
+
+}  // namespace q4gsw

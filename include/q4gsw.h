@@ -63,7 +63,8 @@ typedef enum q4gsw_status {
     Q4GSW_E_HIP = 9,          /* a HIP runtime call or kernel launch failed */
     Q4GSW_E_BUFFER = 10,      /* packed buffer smaller than q4gsw_packed_bytes */
     Q4GSW_E_ROUTE = 11,       /* the route requested in q4gsw_options cannot serve this call */
-    Q4GSW_E_SCRATCH = 12      /* q4gsw_linear_fwd_noalloc: the call needs more than Q4GSW_SCRATCH_BYTES */
+    Q4GSW_E_SCRATCH = 12,     /* q4gsw_linear_fwd_noalloc: the call needs more than Q4GSW_SCRATCH_BYTES */
+    Q4GSW_E_ALIGN = 13        /* a pointer or row pitch that must be a multiple of 16 bytes is not */
 } q4gsw_status;
 
 typedef enum q4gsw_dtype {
@@ -364,6 +365,118 @@ q4gsw_status q4gsw_adamw_step(float *param, const float *grad, float *exp_avg, f
  */
 q4gsw_status q4gsw_embedding(const q4gsw_weight *w, const int64_t *ids, int64_t T, float *out,
                              void *stream);
+
+/*
+ * ---- decoder serving: norm to int8 rows, 4-bit key/value cache, attention over it ----------------
+ *
+ * Rows of int8 activations as an object of their own, so that a norm can write them and several
+ * linears read them.  A rows buffer is device memory of q4gsw_dq8ca_rows_bytes(M, K) bytes, 256-byte
+ * aligned, written whole by q4gsw_rmsnorm_dq8ca for M rows of K columns; its layout is the library's.
+ * E_NULL, E_SHAPE (M or K < 1 or too large).
+ */
+q4gsw_status q4gsw_dq8ca_rows_bytes(int64_t M, int64_t K, uint64_t *bytes);
+
+/*
+ * Residual addition, root-mean-square norm and int8 rows in one pass:
+ *   h = round(x + residual) in r_dtype (x rounded to r_dtype when residual is NULL),
+ *   t = h * weight in fp32;  codes and zero point of each row of t as q4gsw_dq8ca_quantize defines
+ *   them;  row scale = step * fp32(1 / sqrt(mean(h^2) + eps)), the mean in fp64.
+ * The row stands for scale * (code - zero_point), the normalised row times weight in 8 bits.
+ *   x         device [M, K] in x_dtype
+ *   residual  device [M, K] in r_dtype, or NULL;  weight device [K] in r_dtype
+ *   h         device [M, K] in r_dtype, or NULL; may be `residual` itself (updated in place)
+ *   rows      device rows buffer for (M, K), rows_bytes bytes
+ *   values    device fp32 [M, K], or NULL: what the rows stand for
+ * E_NULL, E_SHAPE (M, K; eps negative or not finite), E_DTYPE, E_BUFFER (rows too small),
+ * E_ALIGN (rows not 256-byte aligned), E_ALIAS (an output overlaps an input or another output).
+ */
+q4gsw_status q4gsw_rmsnorm_dq8ca(const void *x, int32_t x_dtype, const void *residual, const void *weight,
+                                 int32_t r_dtype, int64_t M, int64_t K, float eps, void *h, void *rows,
+                                 uint64_t rows_bytes, float *values, void *stream);
+
+/*
+ * q4gsw_linear_dq8ca on rows that are quantised already: y[M, N] (fp32) = rows . dequant(W)^T.
+ *   rows  device rows buffer holding M rows of w->K columns
+ *   ws    device workspace of ws_bytes >= q4gsw_dq8ca_rows_workspace_bytes (may be NULL when that is 0)
+ * E_GROUP, E_BUFFER, E_ALIGN and the errors of q4gsw_linear_dq8ca.
+ */
+q4gsw_status q4gsw_dq8ca_rows_workspace_bytes(const q4gsw_weight *w, int64_t M, uint64_t *bytes);
+q4gsw_status q4gsw_linear_dq8ca_rows(const q4gsw_weight *w, const void *rows, uint64_t rows_bytes, int64_t M,
+                                     float *y, void *ws, uint64_t ws_bytes, void *stream);
+
+/*
+ * A paged cache of keys and values in 4 bits: `pages` pages of page_size tokens (a power of two,
+ * 32..4096) of `heads` heads of `dim` channels (64, 96, 128, 192 or 256).  Per token, head and run of
+ * 32 channels x, every step in fp32 (rint: half to even), NaN counting as 0:
+ *   scale = fp16(min(max|x| / 7, 8188)),  value = clamp(rint(x * (1 / scale)), -8, 7), 0 where scale is 0,
+ * and the cache stands for value * scale: 4.5 bits a channel.
+ * Plain data, filled by the caller; `data` (16-byte aligned, q4gsw_kv_bytes bytes) stays the caller's.
+ */
+typedef struct q4gsw_kv_cache {
+    int64_t pages;
+    int32_t page_size;
+    int32_t heads;
+    int32_t dim;
+    int32_t reserved;         /* 0 */
+    void *data;
+    uint64_t bytes;
+} q4gsw_kv_cache;
+/* Bytes of a cache (data and bytes of `c` are not looked at).  E_NULL, E_SHAPE. */
+q4gsw_status q4gsw_kv_bytes(const q4gsw_kv_cache *c, uint64_t *bytes);
+
+/*
+ * The sequences of a call.  Sequence b owns token rows cu[b] .. cu[b + 1] - 1 of the call's token
+ * arrays (cu device int32 [batch + 1], not decreasing); they are the last of the lens[b] (device int32
+ * [batch]) tokens it has with them.  Its token at place p is in page table[b * table_ld + p / page_size]
+ * (device int32).  A place before 0, past the table's table_cols columns or on a page number outside
+ * [0, pages) is no place: nothing is stored there, it reads as zeros and attention does not see it.
+ * Token rows that belong to no sequence are not touched (attention: left undefined).
+ */
+typedef struct q4gsw_kv_seqs {
+    const int32_t *table;
+    int64_t table_ld;
+    int32_t table_cols;
+    int32_t batch;
+    const int32_t *cu;
+    const int32_t *lens;
+    int64_t tokens;           /* token rows of the call's arrays */
+} q4gsw_kv_seqs;
+
+/*
+ * Store the new tokens' keys and values.
+ *   k, v  device, token rows k_ld / v_ld elements apart, each [heads][dim] dense, in dtype; 16-byte
+ *         aligned, pitches multiples of 16 bytes
+ * Pages written by one call must not be shared by its sequences.  Token rows of 0 launch nothing.
+ * E_NULL, E_SHAPE, E_DTYPE, E_BUFFER (cache too small), E_ALIGN, E_ALIAS (an input overlaps the cache).
+ */
+q4gsw_status q4gsw_kv_append(const q4gsw_kv_cache *c, const q4gsw_kv_seqs *s, const void *k, int64_t k_ld,
+                             const void *v, int64_t v_ld, int32_t dtype, void *stream);
+/* The new tokens' rows back: k, v device fp32 [tokens][heads][dim], 16-byte aligned.  Errors as above. */
+q4gsw_status q4gsw_kv_read(const q4gsw_kv_cache *c, const q4gsw_kv_seqs *s, float *k, float *v, void *stream);
+
+/*
+ * Causal attention of the new tokens over the cache:
+ *   x[t] = q . k[t] / sqrt(dim);  with softcap > 0: x = softcap * tanh(x / softcap);
+ *   out = sum_t softmax(x)[t] v[t] over t <= the token's place and, with window > 0, t > place - window.
+ * A row that sees no key gives zeros.  Query head h reads cache head h / (hq / heads).
+ *   q    device, token rows q_ld elements apart, each [hq][dim] dense, in dtype; 16-byte aligned, pitch a
+ *        multiple of 16 bytes.  Held as fp16 after a power of two per row (exact for fp16 and bf16 down
+ *        to 2^-19 of the row's largest; fp32 rounds to 2^-11)
+ *   out  device [tokens][hq][dim] in dtype, 16-byte aligned
+ *   max_new, max_ctx  bounds of the sequences' new tokens and lengths, for the launch: rows of new
+ *        tokens past max_new are left undefined; a length above max_ctx is served, but slowly
+ *   ws   device workspace of ws_bytes >= q4gsw_kv_attention_workspace_bytes (256-byte aligned; may be
+ *        NULL when that is 0)
+ * Scores, the softmax and all sums are held in fp32; keys, values and weights enter the products as
+ * fp16 (one rounding each).  Results do not depend on the launch.  Tokens of 0 launch nothing.
+ * E_NULL, E_SHAPE (hq not a multiple of heads; sizes; window negative; softcap neither 0 nor in 1e-30..1e30),
+ * E_DTYPE, E_BUFFER, E_ALIGN, E_WORKSPACE, E_ALIAS (out or ws overlaps q, the cache or each other).
+ */
+q4gsw_status q4gsw_kv_attention_workspace_bytes(const q4gsw_kv_cache *c, int32_t batch, int64_t tokens, int32_t hq,
+                                                int32_t max_new, int32_t max_ctx, uint64_t *bytes);
+q4gsw_status q4gsw_kv_attention(const q4gsw_kv_cache *c, const q4gsw_kv_seqs *s, const void *q, int64_t q_ld,
+                                int32_t dtype, int32_t hq, int32_t max_new, int32_t max_ctx, int32_t window,
+                                float softcap, void *out, void *ws, uint64_t ws_bytes, void *stream);
 
 /* Route attestation: the q4gsw_route_id a plain call (no options) with these
  * arguments takes (Q4GSW_ROUTE_NONE if it would fail validation).  For
