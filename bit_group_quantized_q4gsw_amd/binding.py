@@ -168,8 +168,10 @@ def _check(status: int, what: str) -> None:
         raise Q4gswError(status, what)
 
 
-def _stream() -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+def _stream() -> int:
+    """The current device's current stream as the integer a stream argument takes (through torch's raw
+    accessors: building a Stream object costs more than a small kernel's launch)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dev(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -519,10 +521,14 @@ def kv_attention(cache: KvCache, q: torch.Tensor, table: torch.Tensor, cu: torch
     elif out.dtype != q.dtype or out.shape != q.shape or out.device != dev or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {q.dtype} tensor [tokens, hq, dim] on {dev}")
     seqs = _kv_seqs(cache, table, cu, lens, tokens)
-    need = kv_attention_workspace_bytes(cache, seqs.batch, tokens, hq, max_new, max_ctx)
-    ws, wp, wb = _ws_args(need, workspace, dev)
+    if workspace is None:
+        need = kv_attention_workspace_bytes(cache, seqs.batch, tokens, hq, max_new, max_ctx)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
     _check(lib().q4gsw_kv_attention(cache._ref, ctypes.byref(seqs), q.data_ptr(), q_ld, _TORCH_DTYPE[q.dtype], hq, max_new,
-                                    max_ctx, window, softcap, out.data_ptr(), wp, wb, _stream()), "q4gsw_kv_attention")
+                                    max_ctx, window, softcap, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                    _stream()), "q4gsw_kv_attention")
     return out
 
 

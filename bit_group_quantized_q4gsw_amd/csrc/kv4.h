@@ -17,7 +17,7 @@
 //     the keys' rows holds, and half h of a 32x32 product holds in registers 8 u + 4 ab + j, so
 //     the probabilities enter the second product from the registers they were computed in;
 //   * entry k of a word (channel or token slot) is its nibble nib_pos(k); code = value + 8;
-//   * scales are fp16: keys' [i][g][ab] (a lane's row), values' [q][g][slot].
+//   * scales are fp16, keys' and values' alike [q][g][slot]: the scales of the tokens of q.
 #pragma once
 #include "device.h"
 
@@ -90,19 +90,25 @@ __host__ __device__ __forceinline__ constexpr int kv_tok(int q, int slot) {
 // of 2^10 reads 1024 + code, one at bits 4..7 under that of 2^6 reads 64 + code: pairs 0 and 2 are
 // off by 1024 + 8, pairs 1 and 3 by 64 + 8, and one shift serves a word.
 constexpr float kBiasEven = 1032.0f, kBiasOdd = 72.0f;
-__device__ __forceinline__ u4 codes_biased_f16(uint32_t w) {
-    const uint32_t w8 = w >> 8;
-    return u4{(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x54005400u, (w8 & 0x000F000Fu) | 0x64006400u,
-              (w8 & 0x00F000F0u) | 0x54005400u};
-}
-
-// The same word as code - 8, exactly, times the pairs of scales s (rounded to fp16 once).
-__device__ __forceinline__ u4 codes_scaled_f16(uint32_t w, h2 s0, h2 s1, h2 s2, h2 s3) {
-    const u4 b = codes_biased_f16(w);
-    const h2 e = {(_Float16)kBiasEven, (_Float16)kBiasEven}, o = {(_Float16)kBiasOdd, (_Float16)kBiasOdd};
-    return u4{bitcast<uint32_t>((bitcast<h2>(b[0]) - e) * s0), bitcast<uint32_t>((bitcast<h2>(b[1]) - o) * s1),
-              bitcast<uint32_t>((bitcast<h2>(b[2]) - e) * s2), bitcast<uint32_t>((bitcast<h2>(b[3]) - o) * s3)};
-}
+// The constants are held in registers, which makes a pair one v_and_or_b32: 5 VALU a word.
+struct Unpack {
+    uint32_t lo = 0x000F000Fu, hi = 0x00F000F0u, even = 0x64006400u, odd = 0x54005400u;
+    __device__ __forceinline__ Unpack() {
+        asm volatile("" : "+s"(lo), "+s"(hi));
+        asm volatile("" : "+v"(even), "+v"(odd));
+    }
+    __device__ __forceinline__ u4 biased(uint32_t w) const {
+        const uint32_t w8 = w >> 8;
+        return u4{(w & lo) | even, (w & hi) | odd, (w8 & lo) | even, (w8 & hi) | odd};
+    }
+    // code - 8, exactly
+    __device__ __forceinline__ u4 values(uint32_t w) const {
+        const u4 b = biased(w);
+        const h2 e = {(_Float16)kBiasEven, (_Float16)kBiasEven}, o = {(_Float16)kBiasOdd, (_Float16)kBiasOdd};
+        return u4{bitcast<uint32_t>(bitcast<h2>(b[0]) - e), bitcast<uint32_t>(bitcast<h2>(b[1]) - o),
+                  bitcast<uint32_t>(bitcast<h2>(b[2]) - e), bitcast<uint32_t>(bitcast<h2>(b[3]) - o)};
+    }
+};
 
 // Bytes of the unit of (page, head, block in the page).
 __device__ __forceinline__ int64_t kv_unit(const KvView& c, int64_t page, int head, int sub) {

@@ -93,29 +93,50 @@ __device__ __forceinline__ void store4(void* out, int dtype, int64_t e, f4 v) {
     }
 }
 
-// Eight neighbouring channels of a query row (16-byte aligned) as fp32.
-__device__ __forceinline__ void load_q8(const void* q, int dtype, int64_t e, float* v) {
-    if (dtype == kF32) {
-        const f4 a = bitcast<f4>(ldg16(static_cast<const float*>(q) + e));
-        const f4 b = bitcast<f4>(ldg16(static_cast<const float*>(q) + e + 4));
+// A lane's part of a query row as operand fragments: octets at e0 + stride * i, i < N, 16-byte
+// aligned; ok false gives zeros.  All loads are issued together, the row's largest magnitude is
+// joined over the lanes that share the row by `join`, and fp16 pairs times 2^k go to frag.  Returns
+// the factor back, 2^-k.
+template <int DT, int N, class Join>
+__device__ __forceinline__ float load_query(const void* q, int64_t e0, int stride, bool ok, Join join, u4 (&frag)[N]) {
+    constexpr int W = DT == kF32 ? 2 : 1;
+    u4 raw[N * W];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-        return;
-    }
-    const u4 a = ldg16(static_cast<const uint16_t*>(q) + e);
+    for (int i = 0; i < N; ++i) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (dtype == kF16) {
-            v[2 * i] = f16_bits_to_f32((uint16_t)(a[i] & 0xFFFFu));
-            v[2 * i + 1] = f16_bits_to_f32((uint16_t)(a[i] >> 16));
-        } else {
-            v[2 * i] = bitcast<float>(a[i] << 16);
-            v[2 * i + 1] = bitcast<float>(a[i] & 0xFFFF0000u);
+        for (int w = 0; w < W; ++w)
+            raw[i * W + w] = DT == kF32 ? ldg16(static_cast<const float*>(q) + e0 + stride * i + 4 * w)
+                                        : ldg16(static_cast<const uint16_t*>(q) + e0 + stride * i);
+    }
+    auto value = [&](int i, int e) -> float {            // element e (0..7) of octet i
+        if constexpr (DT == kF32) return bitcast<float>(raw[i * 2 + (e >> 2)][e & 3]);
+        else if constexpr (DT == kF16) return (float)bitcast<h2>(raw[i][e >> 1])[e & 1];
+        else return bitcast<float>((e & 1) ? raw[i][e >> 1] & 0xFFFF0000u : raw[i][e >> 1] << 16);
+    };
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(value(i, e)));
+    }
+    float mul, inv;
+    row_factor(ok ? join(amax) : 0.0f, mul, inv);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const h2 p = {(_Float16)(value(i, 2 * e) * mul), (_Float16)(value(i, 2 * e + 1) * mul)};
+            frag[i][e] = ok ? bitcast<uint32_t>(p) : 0u;
         }
     }
+    return inv;
+}
+
+template <int N, class Join>
+__device__ __forceinline__ float load_query(const void* q, int dtype, int64_t e0, int stride, bool ok, Join join, u4 (&frag)[N]) {
+    if (dtype == kF32) return load_query<kF32, N>(q, e0, stride, ok, join, frag);
+    if (dtype == kF16) return load_query<kF16, N>(q, e0, stride, ok, join, frag);
+    return load_query<kBF16, N>(q, e0, stride, ok, join, frag);
 }
 
 // kv_rows.hip: `waves` (4 or 8) per workgroup, tiles of 16 * r rows (r 2 only up to 128 channels).

@@ -124,14 +124,13 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvView c, KvSeqs sq
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w |= code[e] << (4 * nib_pos(e));
                 s_kw[kv_word_off<G>(2 * g + (slot >> 2), 16 * (o & 3) + 4 * q + (slot & 3)) >> 2] = w;
-                if ((o & 3) == 0) s_sc[0][(4 * q + (slot & 3)) * 2 * G + 2 * g + (slot >> 2)] = bitcast<uint16_t>(sh);
             } else {
                 u2 w = {0u, 0u};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e >> 2] |= code[e] << (8 * (e & 3));
                 *reinterpret_cast<u2*>(&s_vc[t * D + 8 * o]) = w;
-                if ((o & 3) == 0) s_sc[1][(q * G + g) * 8 + slot] = bitcast<uint16_t>(sh);
             }
+            if ((o & 3) == 0) s_sc[kv][(q * G + g) * 8 + slot] = bitcast<uint16_t>(sh);
         }
     }
     __syncthreads();
@@ -169,11 +168,10 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvView c, KvSeqs sq
         else if (mask) vw[n] = (vw[n] & ~mask) | word;
     }
     for (int n = tid; n < 32 * G; n += kThreads) {
-        const int i = n / (2 * G);
-        const int tk = kv_tok(i >> 2, 4 * (n & 1) + (i & 3));
-        if (tk >= at.t0 && tk < at.t1) ksc[n] = s_sc[0][n];
-        const int tv = kv_tok(n / (8 * G), n & 7);
-        if (tv >= at.t0 && tv < at.t1) vsc[n] = s_sc[1][n];
+        const int t = kv_tok(n / (8 * G), n & 7);
+        if (t < at.t0 || t >= at.t1) continue;
+        ksc[n] = s_sc[0][n];
+        vsc[n] = s_sc[1][n];
     }
 }
 
@@ -199,7 +197,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvView c, KvSeqs sq, 
         const int64_t dst = ((at.row0 + t) * c.heads + head) * D + 8 * o;
         const uint32_t w =
             *reinterpret_cast<const uint32_t*>(&s_unit[kv_word_off<G>(2 * g + (slot >> 2), 16 * (o & 3) + 4 * q + (slot & 3))]);
-        const float ks = f16_bits_to_f32(ksc[(4 * q + (slot & 3)) * 2 * G + 2 * g + (slot >> 2)]);
+        const float ks = f16_bits_to_f32(ksc[(q * G + g) * 8 + slot]);
         float x[8];
         word_codes_minus8_f32(w, x);
         f4 lo, hi;

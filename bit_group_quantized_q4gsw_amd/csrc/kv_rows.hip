@@ -4,18 +4,20 @@
 //   t > place - window;  out[r] = sum_t softmax(score)[r, t] v[t].
 //
 // Rows are the new tokens of one sequence times the query heads of one head of the cache.  Every
-// wave works alone on 32-token blocks: 4 KB of codes and 0.5 KB of scales per block (dim 128)
-// come straight from memory into the lanes that use them, 16 bytes a lane, one block ahead.
-//   * scores: 16x16x32 MFMA, keys as the first operand, so a lane holds the scores of eight
-//     tokens of one row.  With one tile of rows (R 1) the keys' codes enter as fp16 code + bias,
-//     unpacked by 5 VALU a word; the product starts from -bias * sum(q) and every run of 32
-//     channels is one MFMA, whose fp32 sum is multiplied by the token's scale: exact products.
-//     With two tiles that multiplication would double, and the scale is multiplied into the
-//     unpacked fp16 codes instead (one rounding, 2^-11).
+// wave works alone on 32-token blocks, each a unit of 36 dim bytes that LDS-DMA brings into the
+// wave's own two LDS stages (no registers, no barrier; the next unit loads while one is used).
+//   * scores: 16x16x32 MFMA, keys as the first operand, so a lane holds the scores of eight tokens
+//     of one row.  The codes enter as fp16 integers and every run of 32 channels is one MFMA, whose
+//     fp32 sum is multiplied by the token's scale: exact products (a scale multiplied into fp16
+//     codes would round, and scores feel that rounding most: twice the output's own).  With one
+//     tile of rows of 64 channels the codes keep the bias of their unpacking, which saves 4 of 9
+//     VALU a word, and the product starts from -bias * sum(q) (wider rows have no registers left
+//     to hold that start).
 //   * weights: running reference and sum of a softmax in fp32; the reference moves only when some
 //     score passes it by kSlack, so most blocks need no exchange between lanes and no rescaling.
-//   * sums: 16x16x32 MFMA, values (code - 8) * scale in fp16 (one rounding) as the first operand;
-//     the weights, rounded to fp16, are the second operand as the lane holds them.
+//   * sums: 16x16x32 MFMA, values' codes as the first operand; the second, which the lane holds
+//     already, is weight * scale, one fp16 rounding a run of channels.  The reference carries the
+//     power of two above the largest scale so far (vlog), which keeps the products in fp16's range.
 // The waves of a workgroup join through LDS at the end; splits of the cache's length join in a
 // second launch (kv_join_kernel).
 //
@@ -25,57 +27,36 @@
 namespace q4gsw {
 namespace {
 
-template <int G, int R>
-struct Block {
-    uint32_t k[2 * G], v[2 * G];
-    uint32_t ks[R == 1 ? 4 * G : G];
-    uint32_t vs[4 * G];
-};
+// The next unit into this wave's LDS, 1 KB an instruction.
+template <int D>
+__device__ __forceinline__ void fetch_unit(const uint8_t* unit, lds_u8* dst, int lane) {
+    constexpr int kBytes = 36 * D, kFull = kBytes / 1024, kRest = kBytes % 1024;
+#pragma unroll
+    for (int i = 0; i < kFull; ++i) dma16(unit + 1024 * i + 16 * lane, dst + 1024 * i);
+    if constexpr (kRest != 0) {
+        if (lane < kRest / 16) dma16(unit + 1024 * kFull + 16 * lane, dst + 1024 * kFull);
+    }
+}
 
-// Words 0 .. 2 G - 1 of this lane.
+// Wait until at most N of this wave's vector-memory loads are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Words 2 g and 2 g + 1 of `lane` in a code plane.
 template <int G>
-__device__ __forceinline__ void load_plane(const uint8_t* p, int lane, uint32_t* w) {
-#pragma unroll
-    for (int i = 0; i < G / 2; ++i) {
-        const u4 x = ldg16(p + 1024 * i + 16 * lane);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[4 * i + e] = x[e];
-    }
-    if constexpr (G & 1) {
-        const u2 x = *reinterpret_cast<const u2*>(p + 512 * (G - 1) + 8 * lane);
-        w[2 * G - 2] = x[0];
-        w[2 * G - 1] = x[1];
-    }
+__device__ __forceinline__ u2 word_pair(const uint8_t* plane, int g, int lane) {
+    return *reinterpret_cast<const u2*>(plane + kv_word_off<G>(2 * g, lane));
 }
 
-template <int G, int R>
-__device__ __forceinline__ void load_block(const uint8_t* unit, int lane, Block<G, R>& b) {
-    const int i = lane & 15, q = lane >> 4;
-    load_plane<G>(unit, lane, b.k);
-    const uint8_t* sc = unit + 1024 * G;
-    if constexpr (R == 1) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const u4 x = ldg16(sc + 16 * G * q + 16 * g);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) b.ks[4 * g + e] = x[e];
-        }
-    } else {
-#pragma unroll
-        for (int g = 0; g < G; ++g) b.ks[g] = *reinterpret_cast<const uint32_t*>(sc + 4 * G * i + 4 * g);
-    }
-    load_plane<G>(unit + 512 * G, lane, b.v);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const u4 x = ldg16(sc + 64 * G + 16 * G * q + 16 * g);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b.vs[4 * g + e] = x[e];
-    }
-}
+// Waves a SIMD holds: what the registers allow (sums D / 4 and queries D / 8 per tile of rows).
+constexpr int rows_waves(int D, int R) { return R == 2 ? 2 : (D == 64 ? 4 : (D <= 128 ? 3 : 2)); }
 
 template <int D, int R>
-__global__ __launch_bounds__(512) void kv_rows_kernel(KvAttnArgs a) {
-    constexpr int G = D / 32, C = D / 16;
+__global__ __launch_bounds__(512, rows_waves(D, R)) void kv_rows_kernel(KvAttnArgs a) {
+    constexpr int G = D / 32, C = D / 16, kUnit = 36 * D, kLoads = (kUnit + 1023) / 1024;
+    constexpr bool kBiased = R == 1 && D == 64;
     extern __shared__ __attribute__((aligned(16))) float smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -97,9 +78,34 @@ __global__ __launch_bounds__(512) void kv_rows_kernel(KvAttnArgs a) {
     const int nr = min(16 * R, rows - r0);
     const KvSpan sp = kv_span(a, s, r0, nr, split);
 
+    // ---- the wave's blocks: lo + wave, + waves, ...; page numbers 64 at a time in a register ----
+    const int64_t first = sp.lo + wave;
+    const int64_t left = sp.hi - first;
+    const int n = left > 0 ? (int)((left + waves - 1) / waves) : 0;
+    const int sub_mask = (1 << a.c.bpp_log2) - 1;
+    lds_u8* const ring = (lds_u8*)smem + wave * 2 * kUnit;
+    uint8_t* const ring_r = reinterpret_cast<uint8_t*>(smem) + wave * 2 * kUnit;
+    int pages = -1;
+    // loads block `it` into its stage; false for a page outside the cache (page 0 is loaded instead, so
+    // that every block has the same number of loads)
+    auto fetch = [&](int it) -> bool {
+        const int64_t blk = first + (int64_t)it * waves;
+        if ((it & 63) == 0) {
+            const int64_t mine = first + (int64_t)(it + lane) * waves;
+            pages = mine < sp.hi ? a.sq.table[(int64_t)b * a.sq.table_ld + (mine >> a.c.bpp_log2)] : -1;
+            // used here, so that the wait for it stays on this path and spares the stages in flight
+            asm volatile("" : "+v"(pages));
+        }
+        const int page = __builtin_amdgcn_readlane(pages, it & 63);
+        const bool ok = page >= 0 && page < a.c.pages;
+        fetch_unit<D>(a.c.data + kv_unit(a.c, ok ? page : 0, head, (int)(blk & sub_mask)), ring + (it & 1) * kUnit, lane);
+        return ok;
+    };
+    bool have = n > 0 && fetch(0);
+
     // ---- queries: operand fragments, factors, places ----
     u4 bq[R][G];
-    float cb[R == 1 ? G : 1];            // R 1: -bias * sum of the run's queries
+    float cb[kBiased ? G : 1];           // -bias * sum of the run's queries
     float f[R];
     int pr[R];
 #pragma unroll
@@ -109,37 +115,25 @@ __global__ __launch_bounds__(512) void kv_rows_kernel(KvAttnArgs a) {
         const int tok = ok ? r / a.group : 0, gh = ok ? r - tok * a.group : 0;
         pr[rt] = ok ? s.len - s.m + tok : sp.pmax;
         const int64_t base = (s.first_row + tok) * a.q_ld + (int64_t)(head * a.group + gh) * D;
-        float x[8 * G];
-        float amax = 0.0f;
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            load_q8(a.q, a.dtype, base + 32 * g + 8 * qd, x + 8 * g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[8 * g + e] = ok ? x[8 * g + e] : 0.0f;
-                amax = fmaxf(amax, fabsf(x[8 * g + e]));
-            }
-        }
-        amax = wave_max_rows(amax);
-        float mul, inv;
-        row_factor(amax, mul, inv);
-        f[rt] = a.scale * inv;
+        f[rt] = a.scale * load_query<G>(a.q, a.dtype, base + 8 * qd, 32, ok, wave_max_rows, bq[rt]);
         if (a.cap_out == 0.0f) f[rt] *= kLog2e;
+        if constexpr (kBiased) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            float sum = 0.0f;
+            for (int g = 0; g < G; ++g) {
+                float sum = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const h2 p = {(_Float16)(x[8 * g + 2 * e] * mul), (_Float16)(x[8 * g + 2 * e + 1] * mul)};
-                bq[rt][g][e] = bitcast<uint32_t>(p);
-                if constexpr (R == 1) sum += ((float)p[0] + (float)p[1]) * ((e & 1) ? kBiasOdd : kBiasEven);
+                for (int e = 0; e < 4; ++e) {
+                    const h2 p = bitcast<h2>(bq[rt][g][e]);
+                    sum = fmaf((float)p[0] + (float)p[1], (e & 1) ? kBiasOdd : kBiasEven, sum);
+                }
+                cb[g] = -wave_sum_rows(sum);
             }
-            if constexpr (R == 1) cb[g] = -wave_sum_rows(sum);
         }
     }
 
     f4 o[R][C];
     float mref[R], l[R];
+    float vlog = -40.0f, vlim = 0x1p-40f;    // no scale so far is above vlim = 2^vlog
 #pragma unroll
     for (int rt = 0; rt < R; ++rt) {
         mref[rt] = kNoKey;
@@ -147,35 +141,34 @@ __global__ __launch_bounds__(512) void kv_rows_kernel(KvAttnArgs a) {
 #pragma unroll
         for (int c = 0; c < C; ++c) o[rt][c] = f4{0.f, 0.f, 0.f, 0.f};
     }
+    const Unpack unpack;
+    auto rescale = [&](int rt, float w) {
+        l[rt] *= w;
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[rt][c] *= w;
+    };
 
-    auto compute = [&](const Block<G, R>& bl, int64_t blk) {
+    auto compute = [&](uint8_t* unit, int64_t blk) {
         f4 sc[R][2];
-        if constexpr (R == 1) {
+#pragma unroll
+        for (int rt = 0; rt < R; ++rt) sc[rt][0] = sc[rt][1] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            if (g && (g & 1) == 0 && D * R >= 128) __builtin_amdgcn_sched_barrier(0);
+            const u2 kw = word_pair<G>(unit, g, lane);
+            const u4 ks = *reinterpret_cast<const u4*>(unit + 1024 * G + (qd * G + g) * 16);
 #pragma unroll
             for (int ab = 0; ab < 2; ++ab) {
-                sc[0][ab] = f4{0.f, 0.f, 0.f, 0.f};
+                const u4 kf = kBiased ? unpack.biased(kw[ab]) : unpack.values(kw[ab]);
+                const h2 s01 = bitcast<h2>(ks[2 * ab]), s23 = bitcast<h2>(ks[2 * ab + 1]);
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const f4 p = mfma_f16(codes_biased_f16(bl.k[2 * g + ab]), bq[0][g], f4{cb[g], cb[g], cb[g], cb[g]});
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const h2 ks = bitcast<h2>(bl.ks[j * G + g]);
-                        sc[0][ab][j] = fmaf((float)ks[ab], p[j], sc[0][ab][j]);
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int ab = 0; ab < 2; ++ab) {
-#pragma unroll
-                for (int rt = 0; rt < R; ++rt) sc[rt][ab] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const h2 ks = bitcast<h2>(bl.ks[g]);
-                    const h2 kk = {ks[ab], ks[ab]};
-                    const u4 kf = codes_scaled_f16(bl.k[2 * g + ab], kk, kk, kk, kk);
-#pragma unroll
-                    for (int rt = 0; rt < R; ++rt) sc[rt][ab] = mfma_f16(kf, bq[rt][g], sc[rt][ab]);
+                for (int rt = 0; rt < R; ++rt) {
+                    const float c0 = kBiased ? cb[g] : 0.0f;
+                    const f4 p = mfma_f16(kf, bq[rt][g], f4{c0, c0, c0, c0});
+                    sc[rt][ab][0] = fmaf((float)s01[0], p[0], sc[rt][ab][0]);
+                    sc[rt][ab][1] = fmaf((float)s01[1], p[1], sc[rt][ab][1]);
+                    sc[rt][ab][2] = fmaf((float)s23[0], p[2], sc[rt][ab][2]);
+                    sc[rt][ab][3] = fmaf((float)s23[1], p[3], sc[rt][ab][3]);
                 }
             }
         }
@@ -183,7 +176,39 @@ __global__ __launch_bounds__(512) void kv_rows_kernel(KvAttnArgs a) {
         const int tl = t0 + 16 * (qd >> 1) + 4 * (qd & 1);     // + 8 ab + j
         const bool edge = t0 + 31 > sp.pmin || (a.window && t0 <= sp.pmax - a.window);
         const bool tail = t0 + 32 > s.len;
-        u4 pw[R];
+        if (tail) {
+            // places past the length may hold anything: their values' scales become 0 in the stage
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                u4* const at = reinterpret_cast<u4*>(unit + 1088 * G + (qd * G + g) * 16);
+                u4 vs = *at;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = tl + 8 * (e >> 1) + 2 * (e & 1);
+                    vs[e] = t + 1 < s.len ? vs[e] : (t < s.len ? vs[e] & 0xFFFFu : 0u);
+                }
+                *at = vs;
+            }
+        }
+        auto scales = [&](int g) { return *reinterpret_cast<const u4*>(unit + 1088 * G + (qd * G + g) * 16); };
+        h2 vm = {(_Float16)0.0f, (_Float16)0.0f};
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const u4 vs = scales(g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) vm = __builtin_elementwise_max(vm, bitcast<h2>(vs[e]));
+        }
+        float vmax = fmaxf((float)vm[0], (float)vm[1]);
+        if (__any(vmax > vlim)) {
+            vmax = wave_max_rows(vmax);
+            const int ex = (int)(bitcast<uint32_t>(vmax) >> 23) - 126;     // 2^ex > vmax
+            const float nl = (float)ex;
+#pragma unroll
+            for (int rt = 0; rt < R; ++rt) rescale(rt, __builtin_amdgcn_exp2f(vlog - nl));
+            vlog = nl;
+            vlim = __builtin_amdgcn_exp2f(nl);
+        }
+        float p[R][8];
 #pragma unroll
         for (int rt = 0; rt < R; ++rt) {
             float x[8];
@@ -203,76 +228,62 @@ __global__ __launch_bounds__(512) void kv_rows_kernel(KvAttnArgs a) {
                     x[e] = t <= last && t > gone ? x[e] : -INFINITY;
                 }
             }
-            float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * fl;
+            const float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * fl;
             if (__any(mx > mref[rt] + kSlack)) {
                 const float mn = fmaxf(mref[rt], wave_max_rows(mx));
-                const float w = __builtin_amdgcn_exp2f(mref[rt] - mn);
+                rescale(rt, __builtin_amdgcn_exp2f(mref[rt] - mn));
                 mref[rt] = mn;
-                l[rt] *= w;
-#pragma unroll
-                for (int c = 0; c < C; ++c) o[rt][c] *= w;
             }
-            const float off = kLift - mref[rt];
-            float p[8];
+            const float off = kLift - vlog - mref[rt];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(fmaf(x[e], fl, off));
-            l[rt] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) pw[rt][e] = bitcast<uint32_t>(h2{(_Float16)p[2 * e], (_Float16)p[2 * e + 1]});
+            for (int e = 0; e < 8; ++e) p[rt][e] = __builtin_amdgcn_exp2f(fmaf(x[e], fl, off));
+            l[rt] += ((p[rt][0] + p[rt][1]) + (p[rt][2] + p[rt][3])) + ((p[rt][4] + p[rt][5]) + (p[rt][6] + p[rt][7]));
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            uint32_t vs[4];
+            if (g && (g & 1) == 0 && D * R >= 128) __builtin_amdgcn_sched_barrier(0);
+            const u2 vw = word_pair<G>(unit + 512 * G, g, lane);
+            const u4 vs = scales(g);
+            u4 pw[R];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) vs[e] = bl.vs[4 * g + e];
-            if (tail) {                  // places past the length may hold anything: their values count as 0
+            for (int rt = 0; rt < R; ++rt) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int t = tl + 8 * (e >> 1) + 2 * (e & 1);
-                    vs[e] = t + 1 < s.len ? vs[e] : (t < s.len ? vs[e] & 0xFFFFu : 0u);
+                    const h2 v2 = bitcast<h2>(vs[e]);
+                    const h2 w = {(_Float16)fmaf((float)v2[0], p[rt][2 * e], 0.0f), (_Float16)fmaf((float)v2[1], p[rt][2 * e + 1], 0.0f)};
+                    pw[rt][e] = bitcast<uint32_t>(w);
                 }
             }
 #pragma unroll
-            for (int c = 2 * g; c < 2 * g + 2; ++c) {
-                const u4 vf = codes_scaled_f16(bl.v[c], bitcast<h2>(vs[0]), bitcast<h2>(vs[1]), bitcast<h2>(vs[2]),
-                                               bitcast<h2>(vs[3]));
+            for (int c = 0; c < 2; ++c) {
+                const u4 vf = unpack.values(vw[c]);
 #pragma unroll
-                for (int rt = 0; rt < R; ++rt) o[rt][c] = mfma_f16(vf, pw[rt], o[rt][c]);
+                for (int rt = 0; rt < R; ++rt) o[rt][2 * g + c] = mfma_f16(vf, pw[rt], o[rt][2 * g + c]);
             }
         }
     };
 
-    // ---- the wave's blocks: lo + wave, + waves, ...; page numbers 64 at a time in a register ----
-    const int64_t first = sp.lo + wave;
-    const int64_t left = sp.hi - first;
-    const int64_t n = left > 0 ? (left + waves - 1) / waves : 0;
-    const int sub_mask = (1 << a.c.bpp_log2) - 1;
-    int pages = -1;
-    auto fetch = [&](int64_t it, Block<G, R>& bl) -> bool {
-        if (it >= n) return false;
-        const int64_t blk = first + it * waves;
-        if ((it & 63) == 0) {
-            const int64_t mine = first + (it + lane) * waves;
-            pages = mine < sp.hi ? a.sq.table[(int64_t)b * a.sq.table_ld + (mine >> a.c.bpp_log2)] : -1;
+    for (int it = 0; it < n; ++it) {
+        bool next = false;
+        if (it + 1 < n) {
+            // the stage's last reads are done before new bytes may land in it
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            next = fetch(it + 1);
+            wait_loads<kLoads>();
+        } else {
+            wait_loads<0>();
         }
-        const int page = __builtin_amdgcn_readlane(pages, (int)(it & 63));
-        if (page < 0 || page >= a.c.pages) return false;
-        load_block<G, R>(a.c.data + kv_unit(a.c, page, head, (int)(blk & sub_mask)), lane, bl);
-        return true;
-    };
-    Block<G, R> b0, b1;
-    bool h0 = fetch(0, b0);
-    for (int64_t it = 0; it < n; it += 2) {
-        const bool h1 = fetch(it + 1, b1);
-        if (h0) compute(b0, first + it * waves);
-        h0 = fetch(it + 2, b0);
-        if (h1) compute(b1, first + (it + 1) * waves);
+        if (have) compute(ring_r + (it & 1) * kUnit, first + (int64_t)it * waves);
+        have = next;
     }
+#pragma unroll
+    for (int rt = 0; rt < R; ++rt) mref[rt] += vlog;
 
     // ---- join the waves, one tile of 16 rows after the other ----
     float* const s_ml = smem;                                // [waves][16][2]
     float* const s_o = smem + 32 * waves;                    // [waves][rows of a tile][D + 4]
     const int tile_rows = min(16, a.max_new * a.group);
+    __syncthreads();
 #pragma unroll
     for (int rt = 0; rt < R; ++rt) {
         const int nt = min(16, nr - 16 * rt);
@@ -370,7 +381,8 @@ template <int D>
 static hipError_t rows_launch(const KvAttnArgs& a, int r, int waves, hipStream_t s) {
     const int64_t blocks = (int64_t)a.splits * a.c.heads * a.sq.batch * a.row_tiles;
     const int rows = a.max_new * a.group < 16 ? a.max_new * a.group : 16;
-    const size_t lds = sizeof(float) * (size_t)waves * (32 + (size_t)rows * (D + 4));
+    const size_t join = sizeof(float) * (size_t)waves * (32 + (size_t)rows * (D + 4)), ring = (size_t)waves * 2 * 36 * D;
+    const size_t lds = join > ring ? join : ring;
     const dim3 grid((unsigned)blocks), block(64 * waves);
     if constexpr (D <= 128) {
         if (r == 2) {
