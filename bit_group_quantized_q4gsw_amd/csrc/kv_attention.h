@@ -120,7 +120,8 @@ __device__ __forceinline__ float load_query(const void* q, int64_t e0, int strid
         for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(value(i, e)));
     }
     float mul, inv;
-    row_factor(ok ? join(amax) : 0.0f, mul, inv);
+    amax = join(amax);
+    row_factor(ok ? amax : 0.0f, mul, inv);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
 #pragma unroll
@@ -141,6 +142,8 @@ __device__ __forceinline__ float load_query(const void* q, int dtype, int64_t e0
 
 // kv_rows.hip: `waves` (4 or 8) per workgroup, tiles of 16 * r rows (r 2 only up to 128 channels).
 hipError_t launch_kv_rows(const KvAttnArgs& a, int r, int waves, hipStream_t s);
+// kv_prompt.hip: 32 rows a wave, `waves` 4, or 8 up to 128 channels; a.chunk even.
+hipError_t launch_kv_prompt(const KvAttnArgs& a, int waves, hipStream_t s);
 // The join of the splits' partials into out.
 hipError_t launch_kv_join(const KvAttnArgs& a, hipStream_t s);
 

@@ -66,7 +66,8 @@ uint64_t rows_extent(int64_t tokens, int64_t ld, int64_t row, int es) {
 
 // How an attention call runs.
 struct AttnPlan {
-    int r, waves;                // kv_rows: tiles of 16 r rows, waves per workgroup
+    bool prompt;                 // kv_prompt, else kv_rows
+    int r, waves;                // kv_rows: tiles of 16 r rows; waves per workgroup
     int row_tiles, splits, chunk;
     uint64_t ws_bytes;
 };
@@ -77,21 +78,29 @@ AttnPlan plan_attention(int heads, int dim, int batch, int64_t tokens, int hq, i
     AttnPlan p{};
     const int64_t rows = (int64_t)max_new * (hq / heads);
     int64_t span = max_ctx;
-    if (window && window + (int64_t)max_new + 31 < span) span = window + (int64_t)max_new + 31;
+    if (window && window + (int64_t)max_new + 63 < span) span = window + (int64_t)max_new + 63;
     const int64_t blocks = (span + kKvTok - 1) / kKvTok;
-    p.r = rows > 16 && dim <= 128 ? 2 : 1;
-    p.row_tiles = (int)((rows + 16 * p.r - 1) / (16 * p.r));
-    const int64_t pairs = (int64_t)batch * heads * p.row_tiles;
-    if (blocks <= 16) {
-        p.waves = dim <= 128 ? 8 : 4;
-        p.splits = 1;
+    p.prompt = rows > 64;
+    int64_t want, most;
+    if (p.prompt) {
+        p.waves = dim <= 128 && (int64_t)batch * heads * ((rows + 255) / 256) >= 256 ? 8 : 4;
+        p.row_tiles = (int)((rows + 32 * p.waves - 1) / (32 * p.waves));
+        const int64_t pairs = (int64_t)batch * heads * p.row_tiles;
+        want = (384 + pairs - 1) / pairs;
+        most = (blocks + 15) / 16;
     } else {
-        p.waves = 4;
-        const int64_t want = (3072 + pairs - 1) / pairs, most = (blocks + 15) / 16;
-        p.splits = (int)(want < most ? want : most);
+        p.r = rows > 16 && dim <= 128 ? 2 : 1;
+        p.row_tiles = (int)((rows + 16 * p.r - 1) / (16 * p.r));
+        const int64_t pairs = (int64_t)batch * heads * p.row_tiles;
+        p.waves = blocks <= 16 && dim <= 128 ? 8 : 4;
+        want = (3072 + pairs - 1) / pairs;
+        most = (blocks + 15) / 16;
     }
+    p.splits = (int)(want < most ? want : most);
+    if (p.splits < 1) p.splits = 1;
     p.ws_bytes = p.splits > 1 ? (uint64_t)p.splits * tokens * hq * (dim + 2) * 4 : 0;
     p.chunk = (int)((blocks + p.splits - 1) / p.splits);
+    p.chunk += p.chunk & 1;
     return p;
 }
 
@@ -228,7 +237,7 @@ q4gsw_status q4gsw_kv_attention(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s,
     a.chunk = p.chunk;
     a.row_tiles = p.row_tiles;
     hipStream_t st_ = static_cast<hipStream_t>(stream);
-    hipError_t e = launch_kv_rows(a, p.r, p.waves, st_);
+    hipError_t e = p.prompt ? launch_kv_prompt(a, p.waves, st_) : launch_kv_rows(a, p.r, p.waves, st_);
     if (e == hipSuccess && p.splits > 1) e = launch_kv_join(a, st_);
     return hip_status(e);
 }
