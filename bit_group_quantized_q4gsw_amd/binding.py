@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Tuple
 
@@ -103,7 +104,7 @@ def lib() -> ctypes.CDLL:
         i32, i64, u64, vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
         pw = ctypes.POINTER(WeightDesc)
         po = ctypes.POINTER(Options)
-        pc, ps = ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvSeqs)
+        pc, ps = ctypes.POINTER(KvCacheDesc), vp       # sequences: a KvSeqs by reference or its packed bytes
         sigs = {
             "q4gsw_packed_bytes": [i64, i64, i64, i32, ctypes.POINTER(u64)],
             "q4gsw_pack": [vp, vp, i32, i64, i64, i64, vp, u64, vp, pw],
@@ -380,29 +381,38 @@ def rmsnorm_dq8ca(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: O
     x = _dev(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
-    M, K = x.shape
-    if not weight.is_cuda or tuple(weight.shape) != (K,) or weight.device != x.device or weight.dtype not in _TORCH_DTYPE:
+    shape = x.shape
+    M, K = shape
+    dev = x.get_device()
+    dt = weight.dtype
+    r_dtype = _TORCH_DTYPE.get(dt)
+    if r_dtype is None or weight.dim() != 1 or weight.numel() != K or weight.get_device() != dev:
         raise ValueError(f"weight must be a floating tensor of shape [{K}] on {x.device}")
     weight = weight.contiguous()
-    dt = weight.dtype
+    r_ptr = h_ptr = v_ptr = None
     if residual is not None:
-        if residual.dtype != dt or residual.shape != x.shape or residual.device != x.device:
+        if residual.dtype is not dt or residual.shape != shape or residual.get_device() != dev:
             raise ValueError(f"residual must be {dt} [M, K] on {x.device}")
         residual = residual.contiguous()
+        r_ptr = residual.data_ptr()
         if h is None:
             h = torch.empty_like(residual)
-    if h is not None and (h.dtype != dt or h.shape != x.shape or h.device != x.device or not h.is_contiguous()):
-        raise ValueError(f"h must be a contiguous {dt} tensor [M, K] on {x.device}")
+    if h is not None:
+        if h.dtype is not dt or h.shape != shape or h.get_device() != dev or not h.is_contiguous():
+            raise ValueError(f"h must be a contiguous {dt} tensor [M, K] on {x.device}")
+        h_ptr = h.data_ptr()
     if rows is None:
         rows = dq8ca_rows(M, K, x.device)
-    elif rows.M != M or rows.K != K or rows.buffer.device != x.device:
+    elif rows.M != M or rows.K != K or rows.buffer.get_device() != dev:
         raise ValueError(f"rows must hold [{M}, {K}] on {x.device}")
     if values is not None:
-        _out(values, (M, K), x.device, "values")
-    _check(lib().q4gsw_rmsnorm_dq8ca(
-        x.data_ptr(), _TORCH_DTYPE[x.dtype], residual.data_ptr() if residual is not None else None, weight.data_ptr(),
-        _TORCH_DTYPE[dt], M, K, eps, h.data_ptr() if h is not None else None, rows.buffer.data_ptr(),
-        rows.buffer.numel(), values.data_ptr() if values is not None else None, _stream()), "q4gsw_rmsnorm_dq8ca")
+        if values.dtype is not torch.float32 or values.shape != shape or values.get_device() != dev \
+                or not values.is_contiguous():
+            raise ValueError(f"values must be a contiguous fp32 tensor of shape {list(shape)} on {x.device}")
+        v_ptr = values.data_ptr()
+    buf = rows.buffer
+    _check(lib().q4gsw_rmsnorm_dq8ca(x.data_ptr(), _TORCH_DTYPE[x.dtype], r_ptr, weight.data_ptr(), r_dtype, M, K, eps,
+                                     h_ptr, buf.data_ptr(), buf.numel(), v_ptr, _stream()), "q4gsw_rmsnorm_dq8ca")
     return rows, h, values
 
 
@@ -429,6 +439,7 @@ class KvCache:
         self.buffer = buffer
         self.pages, self.page_size, self.heads, self.dim = desc.pages, desc.page_size, desc.heads, desc.dim
         self._ref = ctypes.byref(desc)
+        self._dev = buffer.get_device()
 
 
 def kv_cache(pages: int, page_size: int, heads: int, dim: int, device="cuda") -> KvCache:
@@ -437,63 +448,80 @@ def kv_cache(pages: int, page_size: int, heads: int, dim: int, device="cuda") ->
     out = ctypes.c_uint64()
     _check(lib().q4gsw_kv_bytes(ctypes.byref(desc), ctypes.byref(out)), "q4gsw_kv_bytes")
     buf = torch.zeros(out.value, dtype=torch.uint8, device=device)
+    if not buf.is_cuda:
+        raise ValueError("a cache lives on a GPU")
     desc.data, desc.bytes = buf.data_ptr(), out.value
     return KvCache(desc, buf)
 
 
-def _kv_seqs(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, tokens: int) -> KvSeqs:
-    dev = cache.buffer.device
-    B = lens.shape[0] if lens.dim() == 1 else -1
-    if lens.dtype != torch.int32 or B < 1 or lens.device != dev or not lens.is_contiguous():
-        raise ValueError(f"lens must be a contiguous int32 tensor [batch] on {dev}")
-    if cu.dtype != torch.int32 or tuple(cu.shape) != (B + 1,) or cu.device != dev or not cu.is_contiguous():
-        raise ValueError(f"cu must be a contiguous int32 tensor [batch + 1] on {dev}")
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B or table.device != dev \
-            or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must be an int32 tensor [batch, pages per sequence] with dense rows on {dev}")
-    cols = table.shape[1]
-    ld = table.stride(0) if B > 1 else cols
-    if ld < cols:
+# q4gsw_kv_seqs as packed bytes: a call's checks and marshalling cost as much as a small kernel, and
+# building a Structure four times what packing its fields does.
+_pack_seqs = struct.Struct("PqiiPPq").pack
+
+
+def _kv_seqs(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, tokens: int) -> bytes:
+    dev, i32 = cache._dev, torch.int32
+    if lens.dtype is not i32 or lens.dim() != 1 or lens.get_device() != dev or not lens.is_contiguous() \
+            or not lens.numel():
+        raise ValueError(f"lens must be a contiguous int32 tensor [batch] on {cache.buffer.device}")
+    B = lens.numel()
+    if cu.dtype is not i32 or cu.dim() != 1 or cu.numel() != B + 1 or cu.get_device() != dev or not cu.is_contiguous():
+        raise ValueError(f"cu must be a contiguous int32 tensor [batch + 1] on {cache.buffer.device}")
+    if table.dtype is not i32 or table.dim() != 2 or table.get_device() != dev:
+        raise ValueError(f"table must be an int32 tensor [batch, pages per sequence] on {cache.buffer.device}")
+    n, cols = table.shape
+    ld, step = table.stride()
+    if n != B or (cols > 1 and step != 1):
+        raise ValueError("table must have a dense row for each sequence")
+    if B == 1:
+        ld = cols
+    elif ld < cols:
         raise ValueError("table's rows must not overlap")
-    return KvSeqs(table.data_ptr(), ld, cols, B, cu.data_ptr(), lens.data_ptr(), tokens)
+    return _pack_seqs(table.data_ptr(), ld, cols, B, cu.data_ptr(), lens.data_ptr(), tokens)
 
 
-def _token_rows(t: torch.Tensor, heads: int, dim: int, device, name: str) -> Tuple[torch.Tensor, int]:
-    """(tensor, token pitch in elements): `t` itself where its token rows are dense and 16-byte
-    aligned (a slice of a fused projection's output, say), else a copy."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.device != device or t.dtype not in _TORCH_DTYPE:
-        raise ValueError(f"{name} must be a floating tensor [tokens, {heads}, {dim}] on {device}")
-    ld = t.stride(0) if t.shape[0] > 1 else heads * dim
-    es = t.element_size()
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim) or ld < heads * dim or (ld * es) % 16 or t.data_ptr() % 16:
+def _token_rows(t: torch.Tensor, heads: int, cache: KvCache, name: str) -> Tuple[torch.Tensor, int, int]:
+    """(tensor, its address, token pitch in elements): `t` itself where its token rows are dense and
+    16-byte aligned (a slice of a fused projection's output, say), else a copy."""
+    dim = cache.dim
+    n, th, td = t.shape if t.dim() == 3 else (0, 0, 0)
+    if th != heads or td != dim or t.get_device() != cache._dev or t.dtype not in _TORCH_DTYPE:
+        raise ValueError(f"{name} must be a floating tensor [tokens, {heads}, {dim}] on {cache.buffer.device}")
+    ld, sh, sd = t.stride()
+    row = heads * dim
+    if n <= 1:
+        ld = row
+    ptr = t.data_ptr()
+    if sd != 1 or (sh != dim and heads > 1) or ld < row or (ptr | ld * t.element_size()) & 15:
         t = t.clone(memory_format=torch.contiguous_format)
-        ld = heads * dim
-    return t, ld
+        return t, t.data_ptr(), row
+    return t, ptr, ld
 
 
 def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, cu: torch.Tensor,
               lens: torch.Tensor) -> None:
     """Store the keys and values k, v [tokens, heads, dim] of new tokens: rows cu[b] .. cu[b + 1] - 1
     are the last of sequence b's lens[b] tokens (with them), whose pages are table[b]."""
-    dev = cache.buffer.device
-    k, k_ld = _token_rows(k, cache.heads, cache.dim, dev, "k")
-    v, v_ld = _token_rows(v, cache.heads, cache.dim, dev, "v")
-    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+    k, kp, k_ld = _token_rows(k, cache.heads, cache, "k")
+    v, vp, v_ld = _token_rows(v, cache.heads, cache, "v")
+    dt = k.dtype
+    tokens = k.shape[0]
+    if v.dtype is not dt or v.shape[0] != tokens:
         raise ValueError("k and v must have one dtype and one number of tokens")
-    seqs = _kv_seqs(cache, table, cu, lens, k.shape[0])
-    _check(lib().q4gsw_kv_append(cache._ref, ctypes.byref(seqs), k.data_ptr(), k_ld, v.data_ptr(), v_ld,
-                                 _TORCH_DTYPE[k.dtype], _stream()), "q4gsw_kv_append")
+    _check(lib().q4gsw_kv_append(cache._ref, _kv_seqs(cache, table, cu, lens, tokens), kp, k_ld, vp, v_ld,
+                                 _TORCH_DTYPE[dt], _stream()), "q4gsw_kv_append")
 
 
 def kv_read(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, tokens: int,
             out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(k, v) fp32 [tokens, heads, dim]: what the cache stands for at the places kv_append with the
     same table, cu and lens writes."""
+    seqs = _kv_seqs(cache, table, cu, lens, tokens)
     dev = cache.buffer.device
     shape = (tokens, cache.heads, cache.dim)
-    k, v = (_out(o, shape, dev, name) for o, name in zip(out if out is not None else (None, None), ("k", "v")))
-    seqs = _kv_seqs(cache, table, cu, lens, tokens)
-    _check(lib().q4gsw_kv_read(cache._ref, ctypes.byref(seqs), k.data_ptr(), v.data_ptr(), _stream()), "q4gsw_kv_read")
+    k, v = out if out is not None else (None, None)
+    k, v = _out(k, shape, dev, "k"), _out(v, shape, dev, "v")
+    _check(lib().q4gsw_kv_read(cache._ref, seqs, k.data_ptr(), v.data_ptr(), _stream()), "q4gsw_kv_read")
     return k, v
 
 
@@ -511,24 +539,25 @@ def kv_attention(cache: KvCache, q: torch.Tensor, table: torch.Tensor, cu: torch
     """out [tokens, hq, dim] of q's dtype: causal attention of the new tokens q over the cache, which
     holds their own keys and values already.  max_new and max_ctx bound the sequences' new tokens and
     lengths; window > 0 keeps the last `window` keys of each token, softcap > 0 caps the scores."""
-    dev = cache.buffer.device
     if q.dim() != 3:
         raise ValueError("q must be [tokens, hq, dim]")
-    tokens, hq = q.shape[0], q.shape[1]
-    q, q_ld = _token_rows(q, hq, cache.dim, dev, "q")
+    shape = q.shape
+    tokens, hq, _ = shape
+    dt = q.dtype
+    q, qp, q_ld = _token_rows(q, hq, cache, "q")
     if out is None:
-        out = torch.empty(tokens, hq, cache.dim, dtype=q.dtype, device=dev)
-    elif out.dtype != q.dtype or out.shape != q.shape or out.device != dev or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous {q.dtype} tensor [tokens, hq, dim] on {dev}")
+        out = torch.empty(shape, dtype=dt, device=q.device)
+    elif out.dtype is not dt or out.shape != shape or out.get_device() != cache._dev or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {dt} tensor [tokens, hq, dim] on {cache.buffer.device}")
     seqs = _kv_seqs(cache, table, cu, lens, tokens)
     if workspace is None:
-        need = kv_attention_workspace_bytes(cache, seqs.batch, tokens, hq, max_new, max_ctx)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
-    _check(lib().q4gsw_kv_attention(cache._ref, ctypes.byref(seqs), q.data_ptr(), q_ld, _TORCH_DTYPE[q.dtype], hq, max_new,
-                                    max_ctx, window, softcap, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                    _stream()), "q4gsw_kv_attention")
+        need = kv_attention_workspace_bytes(cache, lens.numel(), tokens, hq, max_new, max_ctx)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != cache._dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {cache.buffer.device}")
+    _check(lib().q4gsw_kv_attention(cache._ref, seqs, qp, q_ld, _TORCH_DTYPE[dt], hq, max_new, max_ctx, window, softcap,
+                                    out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream()),
+           "q4gsw_kv_attention")
     return out
 
 
