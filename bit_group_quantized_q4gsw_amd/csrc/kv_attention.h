@@ -93,55 +93,68 @@ __device__ __forceinline__ void store4(void* out, int dtype, int64_t e, f4 v) {
     }
 }
 
-// A lane's part of a query row as operand fragments: octets at e0 + stride * i, i < N, 16-byte
-// aligned; ok false gives zeros.  All loads are issued together, the row's largest magnitude is
-// joined over the lanes that share the row by `join`, and fp16 pairs times 2^k go to frag.  Returns
-// the factor back, 2^-k.
-template <int DT, int N, class Join>
-__device__ __forceinline__ float load_query(const void* q, int64_t e0, int stride, bool ok, Join join, u4 (&frag)[N]) {
-    constexpr int W = DT == kF32 ? 2 : 1;
-    u4 raw[N * W];
+// A lane's part of a query row: octets at e0 + stride * i, i < N, 16-byte aligned.  load issues all
+// of its loads together; convert makes operand fragments of them: the row's largest magnitude is
+// joined over the lanes that share the row by `join`, and fp16 pairs times 2^k go to frag (zeros
+// where ok is false).  Returns the factor back, 2^-k.
+template <int N>
+struct QueryRow {
+    u4 raw[2 * N];                       // 16-bit types use the first N
+
+    __device__ __forceinline__ void load(const void* q, int dtype, int64_t e0, int stride) {
+        if (dtype == kF32) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+            for (int i = 0; i < N; ++i) {
+                raw[2 * i] = ldg16(static_cast<const float*>(q) + e0 + stride * i);
+                raw[2 * i + 1] = ldg16(static_cast<const float*>(q) + e0 + stride * i + 4);
+            }
+        } else {
 #pragma unroll
-        for (int w = 0; w < W; ++w)
-            raw[i * W + w] = DT == kF32 ? ldg16(static_cast<const float*>(q) + e0 + stride * i + 4 * w)
-                                        : ldg16(static_cast<const uint16_t*>(q) + e0 + stride * i);
-    }
-    auto value = [&](int i, int e) -> float {            // element e (0..7) of octet i
-        if constexpr (DT == kF32) return bitcast<float>(raw[i * 2 + (e >> 2)][e & 3]);
-        else if constexpr (DT == kF16) return (float)bitcast<h2>(raw[i][e >> 1])[e & 1];
-        else return bitcast<float>((e & 1) ? raw[i][e >> 1] & 0xFFFF0000u : raw[i][e >> 1] << 16);
-    };
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(value(i, e)));
-    }
-    float mul, inv;
-    amax = join(amax);
-    row_factor(ok ? amax : 0.0f, mul, inv);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const h2 p = {(_Float16)(value(i, 2 * e) * mul), (_Float16)(value(i, 2 * e + 1) * mul)};
-            frag[i][e] = ok ? bitcast<uint32_t>(p) : 0u;
+            for (int i = 0; i < N; ++i) raw[i] = ldg16(static_cast<const uint16_t*>(q) + e0 + stride * i);
         }
     }
-    return inv;
-}
 
-template <int N, class Join>
-__device__ __forceinline__ float load_query(const void* q, int dtype, int64_t e0, int stride, bool ok, Join join, u4 (&frag)[N]) {
-    if (dtype == kF32) return load_query<kF32, N>(q, e0, stride, ok, join, frag);
-    if (dtype == kF16) return load_query<kF16, N>(q, e0, stride, ok, join, frag);
-    return load_query<kBF16, N>(q, e0, stride, ok, join, frag);
-}
+    template <int DT, class Join>
+    __device__ __forceinline__ float convert(bool ok, Join join, u4 (&frag)[N]) const {
+        auto value = [&](int i, int e) -> float {            // element e (0..7) of octet i
+            if constexpr (DT == kF32) return bitcast<float>(raw[i * 2 + (e >> 2)][e & 3]);
+            else if constexpr (DT == kF16) return (float)bitcast<h2>(raw[i][e >> 1])[e & 1];
+            else return bitcast<float>((e & 1) ? raw[i][e >> 1] & 0xFFFF0000u : raw[i][e >> 1] << 16);
+        };
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(value(i, e)));
+        }
+        float mul, inv;
+        amax = join(amax);
+        row_factor(ok ? amax : 0.0f, mul, inv);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const h2 p = {(_Float16)(value(i, 2 * e) * mul), (_Float16)(value(i, 2 * e + 1) * mul)};
+                frag[i][e] = ok ? bitcast<uint32_t>(p) : 0u;
+            }
+        }
+        return inv;
+    }
 
-// kv_rows.hip: `waves` (4 or 8) per workgroup, tiles of 16 * r rows (r 2 only up to 128 channels).
-hipError_t launch_kv_rows(const KvAttnArgs& a, int r, int waves, hipStream_t s);
+    template <class Join>
+    __device__ __forceinline__ float convert(int dtype, bool ok, Join join, u4 (&frag)[N]) const {
+        if (dtype == kF32) return convert<kF32>(ok, join, frag);
+        if (dtype == kF16) return convert<kF16>(ok, join, frag);
+        return convert<kBF16>(ok, join, frag);
+    }
+};
+
+// Waves a SIMD holds of the kernel of few rows: what its registers allow (97, 134, 160, 200 and 256
+// for 64 .. 256 channels: sums D / 4, queries D / 8, and their starts).
+constexpr int kv_rows_waves(int D) { return D == 64 ? 4 : (D <= 128 ? 3 : 2); }
+
+// kv_rows.hip: `waves` (4 or 8) per workgroup, tiles of 16 rows.
+hipError_t launch_kv_rows(const KvAttnArgs& a, int waves, hipStream_t s);
 // kv_prompt.hip: 32 rows a wave, `waves` 4, or 8 up to 128 channels; a.chunk even.
 hipError_t launch_kv_prompt(const KvAttnArgs& a, int waves, hipStream_t s);
 // The join of the splits' partials into out.

@@ -31,6 +31,21 @@ __device__ __forceinline__ float sum_halves(float v) {
     return bitcast<float>(r[0]) + bitcast<float>(r[1]);
 }
 
+// Instruction kinds of __builtin_amdgcn_sched_group_barrier
+constexpr int kSchedValu = 0x2, kSchedMfma = 0x8, kSchedRead = 0x100;
+
+// The sequence with `rank` longer ones before it (batches of more than 64: in their order).
+__device__ __forceinline__ int by_length(const KvSeqs& sq, int rank, int lane) {
+    if (sq.batch > 64) return rank;
+    const int mine = lane < sq.batch ? sq.lens[lane] : 0;
+    int before = lane < sq.batch ? 0 : 64;
+    for (int j = 0; j < sq.batch; ++j) {
+        const int other = __builtin_amdgcn_readlane(mine, j);
+        before += other > mine || (other == mine && j < lane);
+    }
+    return __builtin_ctzll(__ballot(before == rank));
+}
+
 // Blocks of 32 tokens in a tile: two, but one where two with remainders do not fit LDS twice.
 constexpr int prompt_blocks(int D, bool prec) { return prec && D > 128 ? 1 : 2; }
 
@@ -46,14 +61,16 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
     const int i = lane & 15, qd = lane >> 4;             // unpacking: lane of a unit
     const int rl = lane & 31, h = lane >> 5;             // products: row or column, half
 
-    // sequence and cache head fastest (one head's row tiles share an XCD's L2), the longest rows first
+    // the longest sequence first, its last rows first, so that the last workgroups to start are short
+    // (three unlike chunks of 2048 rows: 645 -> 620 us); cache heads fastest, so that with eight of them
+    // one head's keys and values stay in one XCD's L2
     int id = blockIdx.x;
-    const int pairs = a.sq.batch * a.c.heads;
-    const int pair = id % pairs;
-    id /= pairs;
+    const int head = id % a.c.heads;
+    id /= a.c.heads;
     const int split = id % a.splits;
-    const int rt0 = a.row_tiles - 1 - id / a.splits;
-    const int head = pair % a.c.heads, b = pair / a.c.heads;
+    id /= a.splits;
+    const int rt0 = a.row_tiles - 1 - id % a.row_tiles;
+    const int b = by_length(a.sq, id / a.row_tiles, lane);
 
     const KvSeq s = kv_seq(a.sq, b);
     const int rows = min(s.m, a.max_new) * a.group;
@@ -76,7 +93,9 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
     float f;
     {
         const int64_t base = (s.first_row + tok) * a.q_ld + (int64_t)(head * a.group + gh) * D;
-        f = a.scale * load_query<S>(a.q, a.dtype, base + 8 * h, 16, ok, max_halves, bq);
+        QueryRow<S> qr;
+        qr.load(a.q, a.dtype, base + 8 * h, 16);
+        f = a.scale * qr.convert(a.dtype, ok, max_halves, bq);
         if (a.cap_out == 0.0f) f *= kLog2e;
     }
 
@@ -179,6 +198,8 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
         f32x16 sc[TB];
 #pragma unroll
         for (int u = 0; u < TB; ++u) sc[u] = zero;
+        // operands are read kAhead products ahead of their use
+        constexpr int kProducts = TB * S * (PREC ? 2 : 1), kAhead = kProducts < 6 ? kProducts : 6;
 #pragma unroll
         for (int k = 0; k < S; ++k) {
 #pragma unroll
@@ -187,6 +208,12 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
                 sc[u] = mfma32_f16(*reinterpret_cast<const u4*>(at), bq[k], sc[u]);
                 if constexpr (PREC) sc[u] = mfma32_f16(*reinterpret_cast<const u4*>(at + 2 * kPlane), bq[k], sc[u]);
             }
+        }
+        __builtin_amdgcn_sched_group_barrier(kSchedRead, kAhead, 0);
+#pragma unroll
+        for (int j = 0; j < kProducts; ++j) {
+            __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+            if (j + kAhead < kProducts) __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
         }
         float fl = f;
         if (a.cap_out != 0.0f) {
@@ -225,26 +252,53 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
             for (int g = 0; g < G; ++g) o[g] *= w;
         }
         const float off = kLift - mref;
+        // 16 tokens a step; a step's operands are read a step ahead, and the weights of the next step
+        // are computed under the products of this one
+        constexpr int kSteps = 2 * TB, kStep = G * (PREC ? 2 : 1);
+        auto operands = [&](int st, u4 (&v)[kStep]) {
 #pragma unroll
-        for (int u = 0; u < TB; ++u) {
+            for (int g = 0; g < G; ++g) {
+                const uint8_t* at = stage + kPlane + ((st >> 1) * S + 2 * g + (st & 1)) * 1024 + 16 * lane;
+                v[g] = *reinterpret_cast<const u4*>(at);
+                if constexpr (PREC) v[G + g] = *reinterpret_cast<const u4*>(at + 2 * kPlane);
+            }
+        };
+        auto weights = [&](int st) -> u4 {
+            u4 p;
+            float sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                u4 p;
-                float sum = 0.0f;
+            for (int e = 0; e < 4; ++e) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(sc[st >> 1][8 * (st & 1) + 2 * e], fl, off));
+                const float y = __builtin_amdgcn_exp2f(fmaf(sc[st >> 1][8 * (st & 1) + 2 * e + 1], fl, off));
+                sum += x + y;
+                p[e] = bitcast<uint32_t>(h2{(_Float16)x, (_Float16)y});
+            }
+            l += sum;
+            return p;
+        };
+        u4 v[2][kStep];
+        operands(0, v[0]);
+        u4 p = weights(0);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = __builtin_amdgcn_exp2f(fmaf(sc[u][8 * w + 2 * e], fl, off));
-                    const float y = __builtin_amdgcn_exp2f(fmaf(sc[u][8 * w + 2 * e + 1], fl, off));
-                    sum += x + y;
-                    p[e] = bitcast<uint32_t>(h2{(_Float16)x, (_Float16)y});
-                }
-                l += sum;
+        for (int st = 0; st < kSteps; ++st) {
+            u4 next = p;
+            if (st + 1 < kSteps) {
+                operands(st + 1, v[(st + 1) & 1]);
+                next = weights(st + 1);
+            }
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const uint8_t* at = stage + kPlane + (u * S + 2 * g + w) * 1024 + 16 * lane;
-                    o[g] = mfma32_f16(*reinterpret_cast<const u4*>(at), p, o[g]);
-                    if constexpr (PREC) o[g] = mfma32_f16(*reinterpret_cast<const u4*>(at + 2 * kPlane), p, o[g]);
-                }
+            for (int j = 0; j < kStep; ++j) o[j % G] = mfma32_f16(v[st & 1][j], p, o[j % G]);
+            p = next;
+        }
+        __builtin_amdgcn_sched_group_barrier(kSchedRead, kStep, 1);
+        __builtin_amdgcn_sched_group_barrier(kSchedValu, 30, 1);
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+            if (st + 1 < kSteps) __builtin_amdgcn_sched_group_barrier(kSchedRead, kStep, 1);
+#pragma unroll
+            for (int j = 0; j < kStep; ++j) {
+                __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 1);
+                if (st + 1 < kSteps) __builtin_amdgcn_sched_group_barrier(kSchedValu, (28 + kStep - 1) / kStep, 1);
             }
         }
     };

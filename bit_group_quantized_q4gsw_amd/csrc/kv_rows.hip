@@ -9,10 +9,9 @@
 //   * scores: 16x16x32 MFMA, keys as the first operand, so a lane holds the scores of eight tokens
 //     of one row.  The codes enter as fp16 integers and every run of 32 channels is one MFMA, whose
 //     fp32 sum is multiplied by the token's scale: exact products (a scale multiplied into fp16
-//     codes would round, and scores feel that rounding most: twice the output's own).  With one
-//     tile of rows of 64 channels the codes keep the bias of their unpacking, which saves 4 of 9
-//     VALU a word, and the product starts from -bias * sum(q) (wider rows have no registers left
-//     to hold that start).
+//     codes would round, and scores feel that rounding most: twice the output's own).  Up to
+//     128 channels the codes keep the bias of their unpacking, which saves 4 of 9 VALU a word, and
+//     the product starts from -bias * sum(q) (wider rows leave no registers to hold that start).
 //   * weights: running reference and sum of a softmax in fp32; the reference moves only when some
 //     score passes it by kSlack, so most blocks need no exchange between lanes and no rescaling.
 //   * sums: 16x16x32 MFMA, values' codes as the first operand; the second, which the lane holds
@@ -50,49 +49,75 @@ __device__ __forceinline__ u2 word_pair(const uint8_t* plane, int g, int lane) {
     return *reinterpret_cast<const u2*>(plane + kv_word_off<G>(2 * g, lane));
 }
 
-// Waves a SIMD holds: what the registers allow (sums D / 4 and queries D / 8 per tile of rows).
-constexpr int rows_waves(int D, int R) { return R == 2 ? 2 : (D == 64 ? 4 : (D <= 128 ? 3 : 2)); }
-
-template <int D, int R>
-__global__ __launch_bounds__(512, rows_waves(D, R)) void kv_rows_kernel(KvAttnArgs a) {
+template <int D>
+__global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnArgs a) {
     constexpr int G = D / 32, C = D / 16, kUnit = 36 * D, kLoads = (kUnit + 1023) / 1024;
-    constexpr bool kBiased = R == 1 && D == 64;
+    constexpr bool kBiased = D <= 128;
     extern __shared__ __attribute__((aligned(16))) float smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int waves = blockDim.x >> 6;
     const int i = lane & 15, qd = lane >> 4;
 
-    int id = blockIdx.x;
+    // Sequences and heads run fastest and each split starts three further on: workgroups go to the
+    // XCDs in turn, so every sequence's splits (the late ones empty in short sequences) reach all of them.
+    const int pairs = a.sq.batch * a.c.heads;
+    const int id = blockIdx.x / pairs;
     const int split = id % a.splits;
-    id /= a.splits;
-    const int head = id % a.c.heads;
-    id /= a.c.heads;
-    const int b = id % a.sq.batch;
-    const int rt0 = id / a.sq.batch;
+    const int rt0 = id / a.splits;
+    const int pair = (int)((blockIdx.x % pairs + 3u * (unsigned)split) % (unsigned)pairs);
+    const int head = pair % a.c.heads, b = pair / a.c.heads;
+
+    // ---- page numbers of the wave's blocks, 64 at a time in a register ----
+    auto page_numbers = [&](int64_t blk) -> int {            // of blocks blk + lane * waves
+        const int64_t col = (blk + (int64_t)lane * waves) >> a.c.bpp_log2;
+        return col < a.sq.table_cols ? a.sq.table[(int64_t)b * a.sq.table_ld + col] : -1;
+    };
+    // without a window the first ones do not wait for the sequence's numbers
+    int pages = -1;
+    if (!a.window) pages = page_numbers((int64_t)split * a.chunk + wave);
 
     const KvSeq s = kv_seq(a.sq, b);
     const int rows = min(s.m, a.max_new) * a.group;
-    const int r0 = rt0 * 16 * R;
+    const int r0 = rt0 * 16;
     if (r0 >= rows) return;
-    const int nr = min(16 * R, rows - r0);
+    const int nr = min(16, rows - r0);
     const KvSpan sp = kv_span(a, s, r0, nr, split);
+    auto out_row = [&](int row) -> int64_t {
+        const int r = r0 + row, tok = r / a.group;
+        return (s.first_row + tok) * a.hq + head * a.group + (r - tok * a.group);
+    };
+    if (sp.hi <= sp.lo && a.splits > 1) {                    // a split past the sequence's end
+        if (tid < nr) {
+            const int64_t prow = (int64_t)split * a.sq.tokens * a.hq + out_row(tid);
+            a.ml[2 * prow] = kNoKey;
+            a.ml[2 * prow + 1] = 0.0f;
+        }
+        return;
+    }
 
-    // ---- the wave's blocks: lo + wave, + waves, ...; page numbers 64 at a time in a register ----
+    // ---- queries and the first block's unit: all loads in flight together ----
+    u4 bq[G];
+    float cb[kBiased ? G : 1];           // -bias * sum of the run's queries
+    const bool ok = i < nr;
+    const int tok = ok ? (r0 + i) / a.group : 0, gh = ok ? r0 + i - tok * a.group : 0;
+    const int place = ok ? s.len - s.m + tok : sp.pmax;
+    QueryRow<G> qr;
+    qr.load(a.q, a.dtype, (s.first_row + tok) * a.q_ld + (int64_t)(head * a.group + gh) * D + 8 * qd, 32);
+
     const int64_t first = sp.lo + wave;
     const int64_t left = sp.hi - first;
     const int n = left > 0 ? (int)((left + waves - 1) / waves) : 0;
     const int sub_mask = (1 << a.c.bpp_log2) - 1;
     lds_u8* const ring = (lds_u8*)smem + wave * 2 * kUnit;
     uint8_t* const ring_r = reinterpret_cast<uint8_t*>(smem) + wave * 2 * kUnit;
-    int pages = -1;
+    if (a.window) pages = page_numbers(first);
     // loads block `it` into its stage; false for a page outside the cache (page 0 is loaded instead, so
     // that every block has the same number of loads)
     auto fetch = [&](int it) -> bool {
         const int64_t blk = first + (int64_t)it * waves;
-        if ((it & 63) == 0) {
-            const int64_t mine = first + (int64_t)(it + lane) * waves;
-            pages = mine < sp.hi ? a.sq.table[(int64_t)b * a.sq.table_ld + (mine >> a.c.bpp_log2)] : -1;
+        if (it && (it & 63) == 0) {
+            pages = page_numbers(blk);
             // used here, so that the wait for it stays on this path and spares the stages in flight
             asm volatile("" : "+v"(pages));
         }
@@ -103,73 +128,51 @@ __global__ __launch_bounds__(512, rows_waves(D, R)) void kv_rows_kernel(KvAttnAr
     };
     bool have = n > 0 && fetch(0);
 
-    // ---- queries: operand fragments, factors, places ----
-    u4 bq[R][G];
-    float cb[kBiased ? G : 1];           // -bias * sum of the run's queries
-    float f[R];
-    int pr[R];
+    float f = a.scale * qr.convert(a.dtype, ok, wave_max_rows, bq);
+    if (a.cap_out == 0.0f) f *= kLog2e;
+    if constexpr (kBiased) {
 #pragma unroll
-    for (int rt = 0; rt < R; ++rt) {
-        const int r = r0 + 16 * rt + i;
-        const bool ok = r < rows;
-        const int tok = ok ? r / a.group : 0, gh = ok ? r - tok * a.group : 0;
-        pr[rt] = ok ? s.len - s.m + tok : sp.pmax;
-        const int64_t base = (s.first_row + tok) * a.q_ld + (int64_t)(head * a.group + gh) * D;
-        f[rt] = a.scale * load_query<G>(a.q, a.dtype, base + 8 * qd, 32, ok, wave_max_rows, bq[rt]);
-        if (a.cap_out == 0.0f) f[rt] *= kLog2e;
-        if constexpr (kBiased) {
+        for (int g = 0; g < G; ++g) {
+            float sum = 0.0f;
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const h2 p = bitcast<h2>(bq[rt][g][e]);
-                    sum = fmaf((float)p[0] + (float)p[1], (e & 1) ? kBiasOdd : kBiasEven, sum);
-                }
-                cb[g] = -wave_sum_rows(sum);
+            for (int e = 0; e < 4; ++e) {
+                const h2 p = bitcast<h2>(bq[g][e]);
+                sum = fmaf((float)p[0] + (float)p[1], (e & 1) ? kBiasOdd : kBiasEven, sum);
             }
+            cb[g] = -wave_sum_rows(sum);
         }
     }
 
-    f4 o[R][C];
-    float mref[R], l[R];
+    f4 o[C];
+    float mref = kNoKey, l = 0.0f;
     float vlog = -40.0f, vlim = 0x1p-40f;    // no scale so far is above vlim = 2^vlog
 #pragma unroll
-    for (int rt = 0; rt < R; ++rt) {
-        mref[rt] = kNoKey;
-        l[rt] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) o[rt][c] = f4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int c = 0; c < C; ++c) o[c] = f4{0.f, 0.f, 0.f, 0.f};
     const Unpack unpack;
-    auto rescale = [&](int rt, float w) {
-        l[rt] *= w;
+    auto rescale = [&](float w) {
+        l *= w;
 #pragma unroll
-        for (int c = 0; c < C; ++c) o[rt][c] *= w;
+        for (int c = 0; c < C; ++c) o[c] *= w;
     };
 
     auto compute = [&](uint8_t* unit, int64_t blk) {
-        f4 sc[R][2];
-#pragma unroll
-        for (int rt = 0; rt < R; ++rt) sc[rt][0] = sc[rt][1] = f4{0.f, 0.f, 0.f, 0.f};
+        f4 sc[2];
+        sc[0] = sc[1] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if (g && (g & 1) == 0 && D * R >= 128) __builtin_amdgcn_sched_barrier(0);
+            if (g && (g & 1) == 0 && D >= 128) __builtin_amdgcn_sched_barrier(0);
             const u2 kw = word_pair<G>(unit, g, lane);
             const u4 ks = *reinterpret_cast<const u4*>(unit + 1024 * G + (qd * G + g) * 16);
+            const float c0 = kBiased ? cb[g] : 0.0f;
 #pragma unroll
             for (int ab = 0; ab < 2; ++ab) {
                 const u4 kf = kBiased ? unpack.biased(kw[ab]) : unpack.values(kw[ab]);
                 const h2 s01 = bitcast<h2>(ks[2 * ab]), s23 = bitcast<h2>(ks[2 * ab + 1]);
-#pragma unroll
-                for (int rt = 0; rt < R; ++rt) {
-                    const float c0 = kBiased ? cb[g] : 0.0f;
-                    const f4 p = mfma_f16(kf, bq[rt][g], f4{c0, c0, c0, c0});
-                    sc[rt][ab][0] = fmaf((float)s01[0], p[0], sc[rt][ab][0]);
-                    sc[rt][ab][1] = fmaf((float)s01[1], p[1], sc[rt][ab][1]);
-                    sc[rt][ab][2] = fmaf((float)s23[0], p[2], sc[rt][ab][2]);
-                    sc[rt][ab][3] = fmaf((float)s23[1], p[3], sc[rt][ab][3]);
-                }
+                const f4 p = mfma_f16(kf, bq[g], f4{c0, c0, c0, c0});
+                sc[ab][0] = fmaf((float)s01[0], p[0], sc[ab][0]);
+                sc[ab][1] = fmaf((float)s01[1], p[1], sc[ab][1]);
+                sc[ab][2] = fmaf((float)s23[0], p[2], sc[ab][2]);
+                sc[ab][3] = fmaf((float)s23[1], p[3], sc[ab][3]);
             }
         }
         const int t0 = (int)(32 * blk);
@@ -191,75 +194,63 @@ __global__ __launch_bounds__(512, rows_waves(D, R)) void kv_rows_kernel(KvAttnAr
             }
         }
         auto scales = [&](int g) { return *reinterpret_cast<const u4*>(unit + 1088 * G + (qd * G + g) * 16); };
-        h2 vm = {(_Float16)0.0f, (_Float16)0.0f};
+        us2 vm = {0, 0};                 // scales are not negative: their bits order like their values
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const u4 vs = scales(g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) vm = __builtin_elementwise_max(vm, bitcast<h2>(vs[e]));
+            for (int e = 0; e < 4; ++e) vm = __builtin_elementwise_max(vm, bitcast<us2>(vs[e]));
         }
-        float vmax = fmaxf((float)vm[0], (float)vm[1]);
+        float vmax = f16_bits_to_f32(vm[0] > vm[1] ? vm[0] : vm[1]);
         if (__any(vmax > vlim)) {
             vmax = wave_max_rows(vmax);
             const int ex = (int)(bitcast<uint32_t>(vmax) >> 23) - 126;     // 2^ex > vmax
             const float nl = (float)ex;
-#pragma unroll
-            for (int rt = 0; rt < R; ++rt) rescale(rt, __builtin_amdgcn_exp2f(vlog - nl));
+            rescale(__builtin_amdgcn_exp2f(vlog - nl));
             vlog = nl;
             vlim = __builtin_amdgcn_exp2f(nl);
         }
-        float p[R][8];
+        float x[8], p[8];
 #pragma unroll
-        for (int rt = 0; rt < R; ++rt) {
-            float x[8];
+        for (int e = 0; e < 8; ++e) x[e] = sc[e >> 2][e & 3];
+        float fl = f;
+        if (a.cap_out != 0.0f) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = sc[rt][e >> 2][e & 3];
-            float fl = f[rt];
-            if (a.cap_out != 0.0f) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = capped_log2(x[e] * fl, a.cap_in, a.cap_out);
-                fl = 1.0f;
-            }
-            if (edge) {
-                const int last = pr[rt], gone = a.window ? pr[rt] - a.window : -1;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int t = tl + 8 * (e >> 2) + (e & 3);
-                    x[e] = t <= last && t > gone ? x[e] : -INFINITY;
-                }
-            }
-            const float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * fl;
-            if (__any(mx > mref[rt] + kSlack)) {
-                const float mn = fmaxf(mref[rt], wave_max_rows(mx));
-                rescale(rt, __builtin_amdgcn_exp2f(mref[rt] - mn));
-                mref[rt] = mn;
-            }
-            const float off = kLift - vlog - mref[rt];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[rt][e] = __builtin_amdgcn_exp2f(fmaf(x[e], fl, off));
-            l[rt] += ((p[rt][0] + p[rt][1]) + (p[rt][2] + p[rt][3])) + ((p[rt][4] + p[rt][5]) + (p[rt][6] + p[rt][7]));
+            for (int e = 0; e < 8; ++e) x[e] = capped_log2(x[e] * fl, a.cap_in, a.cap_out);
+            fl = 1.0f;
         }
+        if (edge) {
+            const int gone = a.window ? place - a.window : -1;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int t = tl + 8 * (e >> 2) + (e & 3);
+                x[e] = t <= place && t > gone ? x[e] : -INFINITY;
+            }
+        }
+        const float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * fl;
+        if (__any(mx > mref + kSlack)) {
+            const float mn = fmaxf(mref, wave_max_rows(mx));
+            rescale(__builtin_amdgcn_exp2f(mref - mn));
+            mref = mn;
+        }
+        const float off = kLift - vlog - mref;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(fmaf(x[e], fl, off));
+        l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if (g && (g & 1) == 0 && D * R >= 128) __builtin_amdgcn_sched_barrier(0);
+            if (g && (g & 1) == 0 && D >= 128) __builtin_amdgcn_sched_barrier(0);
             const u2 vw = word_pair<G>(unit + 512 * G, g, lane);
             const u4 vs = scales(g);
-            u4 pw[R];
+            u4 pw;
 #pragma unroll
-            for (int rt = 0; rt < R; ++rt) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const h2 v2 = bitcast<h2>(vs[e]);
-                    const h2 w = {(_Float16)fmaf((float)v2[0], p[rt][2 * e], 0.0f), (_Float16)fmaf((float)v2[1], p[rt][2 * e + 1], 0.0f)};
-                    pw[rt][e] = bitcast<uint32_t>(w);
-                }
+            for (int e = 0; e < 4; ++e) {
+                const h2 v2 = bitcast<h2>(vs[e]);
+                const h2 w = {(_Float16)fmaf((float)v2[0], p[2 * e], 0.0f), (_Float16)fmaf((float)v2[1], p[2 * e + 1], 0.0f)};
+                pw[e] = bitcast<uint32_t>(w);
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const u4 vf = unpack.values(vw[c]);
-#pragma unroll
-                for (int rt = 0; rt < R; ++rt) o[rt][2 * g + c] = mfma_f16(vf, pw[rt], o[rt][2 * g + c]);
-            }
+            for (int c = 0; c < 2; ++c) o[2 * g + c] = mfma_f16(unpack.values(vw[c]), pw, o[2 * g + c]);
         }
     };
 
@@ -276,100 +267,106 @@ __global__ __launch_bounds__(512, rows_waves(D, R)) void kv_rows_kernel(KvAttnAr
         if (have) compute(ring_r + (it & 1) * kUnit, first + (int64_t)it * waves);
         have = next;
     }
-#pragma unroll
-    for (int rt = 0; rt < R; ++rt) mref[rt] += vlog;
+    mref += vlog;
 
-    // ---- join the waves, one tile of 16 rows after the other ----
+    // ---- join the waves ----
     float* const s_ml = smem;                                // [waves][16][2]
     float* const s_o = smem + 32 * waves;                    // [waves][rows of a tile][D + 4]
     const int tile_rows = min(16, a.max_new * a.group);
+    const float lsum = wave_sum_rows(l);
     __syncthreads();
+    if (qd == 0) {
+        s_ml[2 * (16 * wave + i)] = mref;
+        s_ml[2 * (16 * wave + i) + 1] = lsum;
+    }
+    if (i < nr) {
 #pragma unroll
-    for (int rt = 0; rt < R; ++rt) {
-        const int nt = min(16, nr - 16 * rt);
-        if (nt <= 0) break;
-        if (rt) __syncthreads();
-        const float lsum = wave_sum_rows(l[rt]);
-        if (qd == 0) {
-            s_ml[2 * (16 * wave + i)] = mref[rt];
-            s_ml[2 * (16 * wave + i) + 1] = lsum;
+        for (int c = 0; c < C; ++c)
+            *reinterpret_cast<f4*>(&s_o[(wave * tile_rows + i) * (D + 4) + 16 * c + 4 * qd]) = o[c];
+    }
+    __syncthreads();
+    for (int e = tid; e < nr * (D / 4); e += blockDim.x) {
+        const int row = e / (D / 4), c4 = e - row * (D / 4);
+        float m = kNoKey;
+        for (int w = 0; w < waves; ++w) m = fmaxf(m, s_ml[2 * (16 * w + row)]);
+        float ls = 0.0f;
+        f4 acc = {0.f, 0.f, 0.f, 0.f};
+        for (int w = 0; w < waves; ++w) {
+            const float wt = __builtin_amdgcn_exp2f(s_ml[2 * (16 * w + row)] - m);
+            ls = fmaf(wt, s_ml[2 * (16 * w + row) + 1], ls);
+            acc += wt * *reinterpret_cast<const f4*>(&s_o[(w * tile_rows + row) * (D + 4) + 4 * c4]);
         }
-        if (i < nt) {
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-                *reinterpret_cast<f4*>(&s_o[(wave * tile_rows + i) * (D + 4) + 16 * c + 4 * qd]) = o[rt][c];
-        }
-        __syncthreads();
-        for (int e = tid; e < nt * (D / 4); e += blockDim.x) {
-            const int row = e / (D / 4), c4 = e - row * (D / 4);
-            float m = kNoKey;
-            for (int w = 0; w < waves; ++w) m = fmaxf(m, s_ml[2 * (16 * w + row)]);
-            float ls = 0.0f;
-            f4 acc = {0.f, 0.f, 0.f, 0.f};
-            for (int w = 0; w < waves; ++w) {
-                const float wt = __builtin_amdgcn_exp2f(s_ml[2 * (16 * w + row)] - m);
-                ls = fmaf(wt, s_ml[2 * (16 * w + row) + 1], ls);
-                acc += wt * *reinterpret_cast<const f4*>(&s_o[(w * tile_rows + row) * (D + 4) + 4 * c4]);
-            }
-            const int r = r0 + 16 * rt + row, tok = r / a.group;
-            const int64_t orow = (s.first_row + tok) * a.hq + head * a.group + (r - tok * a.group);
-            if (a.splits == 1) {
-                // a row that no key is seen by has a sum of exactly 0 and gives zeros
-                const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-                store4(a.out, a.dtype, orow * D + 4 * c4, acc * inv);
-            } else {
-                const int64_t prow = (int64_t)split * a.sq.tokens * a.hq + orow;
-                *reinterpret_cast<f4*>(a.part + prow * D + 4 * c4) = acc;
-                if (c4 == 0) {
-                    a.ml[2 * prow] = m;
-                    a.ml[2 * prow + 1] = ls;
-                }
+        const int64_t orow = out_row(row);
+        if (a.splits == 1) {
+            // a row that no key is seen by has a sum of exactly 0 and gives zeros
+            const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+            store4(a.out, a.dtype, orow * D + 4 * c4, acc * inv);
+        } else {
+            const int64_t prow = (int64_t)split * a.sq.tokens * a.hq + orow;
+            *reinterpret_cast<f4*>(a.part + prow * D + 4 * c4) = acc;
+            if (c4 == 0) {
+                a.ml[2 * prow] = m;
+                a.ml[2 * prow + 1] = ls;
             }
         }
     }
 }
 
-// out[row] = sum_s 2^(m_s - m) part_s / sum_s 2^(m_s - m) l_s, in split order per thread and then
-// over the threads' fixed order.  A split that saw no key (l 0) is not read.
+// out[row] = sum_s 2^(m_s - m) part_s / sum_s 2^(m_s - m) l_s: a thread takes every kPar-th split,
+// kBatch of them in flight, on a running reference of its own, and the threads of a channel join in
+// a fixed order.  A split that saw no key (l 0) wrote no sums: what stands there is loaded but not used.
 template <int D>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs a) {
-    constexpr int kQuads = D / 4, kPar = 256 / kQuads;
-    __shared__ float s_red[4];
+    constexpr int kQuads = D / 4, kPar = 256 / kQuads, kBatch = 4;
     __shared__ __attribute__((aligned(16))) f4 s_acc[kPar * kQuads];
-    __shared__ float s_l[kPar];
+    __shared__ float s_l[kPar], s_m[kPar];
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x, rows = a.sq.tokens * a.hq;
     const f4* part = reinterpret_cast<const f4*>(a.part);
     const u2* ml = reinterpret_cast<const u2*>(a.ml);
-    float m = kNoKey;
-    for (int sp = tid; sp < a.splits; sp += 256) m = fmaxf(m, bitcast<float>(ml[sp * rows + row][0]));
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-    if ((tid & 63) == 0) s_red[tid >> 6] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
     const int c4 = tid % kQuads, p = tid / kQuads;
     if (p < kPar) {
         f4 acc = {0.f, 0.f, 0.f, 0.f};
-        float ls = 0.0f;
-        for (int sp = p; sp < a.splits; sp += kPar) {
-            const u2 x = ml[sp * rows + row];
-            const float lw = bitcast<float>(x[1]);
-            if (lw == 0.0f) continue;
-            const float w = __builtin_amdgcn_exp2f(bitcast<float>(x[0]) - m);
-            ls = fmaf(w, lw, ls);
-            acc += w * part[(sp * rows + row) * kQuads + c4];
+        float ls = 0.0f, m = kNoKey;
+        for (int sp = p; sp < a.splits; sp += kBatch * kPar) {
+            u2 x[kBatch];
+            f4 v[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int64_t at = min(sp + j * kPar, a.splits - 1) * rows + row;
+                x[j] = ml[at];
+                v[j] = part[at * kQuads + c4];
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const float lw = bitcast<float>(x[j][1]);
+                if (sp + j * kPar >= a.splits || lw == 0.0f) continue;
+                const float mw = bitcast<float>(x[j][0]), mn = fmaxf(m, mw);
+                const float keep = __builtin_amdgcn_exp2f(m - mn), w = __builtin_amdgcn_exp2f(mw - mn);
+                m = mn;
+                ls = fmaf(w, lw, ls * keep);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] = fmaf(w, v[j][e], acc[e] * keep);
+            }
         }
         s_acc[p * kQuads + c4] = acc;
-        if (c4 == 0) s_l[p] = ls;
+        if (c4 == 0) {
+            s_l[p] = ls;
+            s_m[p] = m;
+        }
     }
     __syncthreads();
     if (tid >= kQuads) return;
-    f4 acc = s_acc[tid];
-    float ls = s_l[0];
-    for (int j = 1; j < kPar; ++j) {
-        acc += s_acc[j * kQuads + tid];
-        ls += s_l[j];
+    float m = kNoKey, ls = 0.0f;
+    f4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kPar; ++j) m = fmaxf(m, s_m[j]);
+#pragma unroll
+    for (int j = 0; j < kPar; ++j) {
+        const float w = __builtin_amdgcn_exp2f(s_m[j] - m);
+        ls = fmaf(w, s_l[j], ls);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = fmaf(w, s_acc[j * kQuads + tid][e], acc[e]);
     }
     const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
     store4(a.out, a.dtype, row * D + 4 * tid, acc * inv);
@@ -378,29 +375,22 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs a) {
 }  // namespace
 
 template <int D>
-static hipError_t rows_launch(const KvAttnArgs& a, int r, int waves, hipStream_t s) {
+static hipError_t rows_launch(const KvAttnArgs& a, int waves, hipStream_t s) {
     const int64_t blocks = (int64_t)a.splits * a.c.heads * a.sq.batch * a.row_tiles;
     const int rows = a.max_new * a.group < 16 ? a.max_new * a.group : 16;
     const size_t join = sizeof(float) * (size_t)waves * (32 + (size_t)rows * (D + 4)), ring = (size_t)waves * 2 * 36 * D;
     const size_t lds = join > ring ? join : ring;
-    const dim3 grid((unsigned)blocks), block(64 * waves);
-    if constexpr (D <= 128) {
-        if (r == 2) {
-            hipLaunchKernelGGL((kv_rows_kernel<D, 2>), grid, block, lds, s, a);
-            return hipGetLastError();
-        }
-    }
-    hipLaunchKernelGGL((kv_rows_kernel<D, 1>), grid, block, lds, s, a);
+    hipLaunchKernelGGL((kv_rows_kernel<D>), dim3((unsigned)blocks), dim3(64 * waves), lds, s, a);
     return hipGetLastError();
 }
 
-hipError_t launch_kv_rows(const KvAttnArgs& a, int r, int waves, hipStream_t s) {
+hipError_t launch_kv_rows(const KvAttnArgs& a, int waves, hipStream_t s) {
     switch (a.c.dim) {
-        case 64: return rows_launch<64>(a, r, waves, s);
-        case 96: return rows_launch<96>(a, r, waves, s);
-        case 128: return rows_launch<128>(a, r, waves, s);
-        case 192: return rows_launch<192>(a, r, waves, s);
-        case 256: return rows_launch<256>(a, r, waves, s);
+        case 64: return rows_launch<64>(a, waves, s);
+        case 96: return rows_launch<96>(a, waves, s);
+        case 128: return rows_launch<128>(a, waves, s);
+        case 192: return rows_launch<192>(a, waves, s);
+        case 256: return rows_launch<256>(a, waves, s);
         default: return hipErrorInvalidValue;
     }
 }

@@ -67,41 +67,98 @@ uint64_t rows_extent(int64_t tokens, int64_t ld, int64_t row, int es) {
 // How an attention call runs.
 struct AttnPlan {
     bool prompt;                 // kv_prompt, else kv_rows
-    int r, waves;                // kv_rows: tiles of 16 r rows; waves per workgroup
+    int waves;                   // per workgroup
     int row_tiles, splits, chunk;
-    uint64_t ws_bytes;
+    float us;                    // estimate
 };
 
-// The splits grow with the span of keys, so a window never needs more workspace than the plan
-// without one.
-AttnPlan plan_attention(int heads, int dim, int batch, int64_t tokens, int hq, int max_new, int max_ctx, int window) {
-    AttnPlan p{};
-    const int64_t rows = (int64_t)max_new * (hq / heads);
-    int64_t span = max_ctx;
-    if (window && window + (int64_t)max_new + 63 < span) span = window + (int64_t)max_new + 63;
-    const int64_t blocks = (span + kKvTok - 1) / kKvTok;
-    p.prompt = rows > 64;
-    int64_t want, most;
-    if (p.prompt) {
-        p.waves = dim <= 128 && (int64_t)batch * heads * ((rows + 255) / 256) >= 256 ? 8 : 4;
-        p.row_tiles = (int)((rows + 32 * p.waves - 1) / (32 * p.waves));
-        const int64_t pairs = (int64_t)batch * heads * p.row_tiles;
-        want = (384 + pairs - 1) / pairs;
-        most = (blocks + 15) / 16;
-    } else {
-        p.r = rows > 16 && dim <= 128 ? 2 : 1;
-        p.row_tiles = (int)((rows + 16 * p.r - 1) / (16 * p.r));
-        const int64_t pairs = (int64_t)batch * heads * p.row_tiles;
-        p.waves = blocks <= 16 && dim <= 128 ? 8 : 4;
-        want = (3072 + pairs - 1) / pairs;
-        most = (blocks + 15) / 16;
-    }
-    p.splits = (int)(want < most ? want : most);
-    if (p.splits < 1) p.splits = 1;
-    p.ws_bytes = p.splits > 1 ? (uint64_t)p.splits * tokens * hq * (dim + 2) * 4 : 0;
-    p.chunk = (int)((blocks + p.splits - 1) / p.splits);
+struct AttnSize {
+    int heads, dim, batch, rows; // rows: new tokens times query heads of a cache head
+    int64_t blocks;              // of 32 keys that some row may see
+    float mean;                  // of them that a row sees
+    bool prec;                   // kv_prompt keeps the remainders of keys and values
+};
+
+constexpr int kCus = 256;
+
+void finish_plan(AttnPlan& p, const AttnSize& n, int64_t splits) {
+    p.splits = (int)(splits < 1 ? 1 : splits);
+    p.chunk = (int)((n.blocks + p.splits - 1) / p.splits);
     p.chunk += p.chunk & 1;
+    // the join: its launch, and the partials written and read at some 4 TB/s
+    p.us = p.splits > 1 ? 3.0f + 2e-6f * p.splits * n.batch * n.heads * n.rows * n.dim : 0.0f;
+}
+
+// Few rows.  The splits of the keys fill the workgroups that fit the GPU at once (32 sequences of
+// 1024 .. 4096 tokens, 8 heads of 128: 3 splits 31.5 us, 8 splits 34.7; two of 131072: 48 splits 58
+// us, 192 splits 73), but a split has 8 blocks, and 16 blocks are not split at all: the join's
+// launch costs more (509 tokens, heads of 64: 6.6 us, 2 splits 8.5; four of 1024, heads of 128: 10.9 us,
+// 4 splits 9.4).  Where that leaves long
+// splits and few turns, unlike lengths end at unlike times, and shorter splits balance them (64
+// sequences of 4096 .. 16384: 1 split 209 us, 8 splits 151).  Eight waves serve a grid of less than
+// a workgroup per CU (509 tokens: 6.6 us against 7.1; 1024 workgroups of 512 tokens: 15.4 against 11.6).
+AttnPlan plan_rows(const AttnSize& n) {
+    AttnPlan p{};
+    p.row_tiles = (n.rows + 15) / 16;
+    const int64_t groups = (int64_t)n.batch * n.heads * p.row_tiles, fit = kCus * kv_rows_waves(n.dim);
+    int64_t splits = 1;
+    if (n.blocks > 16) {
+        splits = fit / groups < n.blocks / 8 ? fit / groups : n.blocks / 8;
+        if (splits < 1) splits = 1;
+        if (n.blocks > 96 * splits && groups < 4 * fit) splits = (n.blocks + 63) / 64;
+    }
+    finish_plan(p, n, splits);
+    p.waves = groups * p.splits < kCus ? 8 : 4;
+    p.us += 6.0f + (0.15f + 0.65f * n.dim / 128) * groups * n.mean / (4 * kCus);
     return p;
+}
+
+// Many rows: eight waves share a tile's unpacking where that still gives every CU a workgroup
+// (wider heads have registers for one wave a SIMD).
+AttnPlan plan_prompt(const AttnSize& n) {
+    AttnPlan p{};
+    p.prompt = true;
+    p.waves = n.dim <= 128 && (int64_t)n.batch * n.heads * ((n.rows + 255) / 256) >= kCus ? 8 : 4;
+    p.row_tiles = (n.rows + 32 * p.waves - 1) / (32 * p.waves);
+    const int64_t groups = (int64_t)n.batch * n.heads * p.row_tiles;
+    const int64_t fill = (kCus * 3 / 2 + groups - 1) / groups, most = (n.blocks + 15) / 16;
+    finish_plan(p, n, fill < most ? fill : most);
+    // 64 keys are a turn; a workgroup's own turns, and all turns over the CUs (two groups of four waves each)
+    const float longest = (n.dim <= 128 ? 3.3f : 9.0f) * 0.5f * p.chunk;
+    const float all = (1.0f + 1.6f * n.dim / 128) * 0.5f * groups * n.mean / (kCus * (p.waves == 8 ? 1 : 2));
+    p.us += 8.0f + (n.prec ? 1.5f : 1.0f) * (longest > all ? longest : all);
+    return p;
+}
+
+AttnSize attention_size(int heads, int dim, int batch, int hq, int max_new, int max_ctx, int window, int dtype) {
+    AttnSize n{heads, dim, batch, max_new * (hq / heads), 0, 0.0f, dtype != kBF16};
+    int64_t span = max_ctx;
+    float mean = max_ctx > max_new ? max_ctx - 0.5f * max_new : 0.5f * max_ctx;
+    if (window) {
+        // the first row's window may begin and the last row's end inside a block
+        if (window + (int64_t)max_new + 30 < span) span = window + (int64_t)max_new + 30;
+        if (window + 32.0f < mean) mean = window + 32.0f;
+    }
+    n.blocks = (span + kKvTok - 1) / kKvTok;
+    n.mean = mean / kKvTok;
+    return n;
+}
+
+// Many rows share a tile's unpacking but take 64 keys in turn after turn, few rows spread over the
+// GPU; which is faster is estimated from the keys a row sees, with the times of one turn and of one
+// tile of 16 rows by 32 keys on the busy GPU (prompts of 32 / 8 heads of 128 from their beginning, few
+// against many rows: 512 tokens 18 against 23 us, 1024 tokens 40 against 56, 2048 tokens 111 against
+// 127, two of 2048 tokens 203 against 94; 1024 tokens behind 7000: 367 against 185).  Up to 32 rows
+// never fill the workgroup of many.
+AttnPlan plan_attention(const AttnSize& n) {
+    const AttnPlan few = plan_rows(n);
+    if (n.rows <= 32) return few;
+    const AttnPlan many = plan_prompt(n);
+    return many.us < few.us ? many : few;
+}
+
+uint64_t plan_workspace(const AttnPlan& p, int64_t tokens, int hq, int dim) {
+    return p.splits > 1 ? (uint64_t)p.splits * tokens * hq * (dim + 2) * 4 : 0;
 }
 
 q4gsw_status check_attention(const q4gsw_kv_cache* c, int64_t batch, int64_t tokens, int32_t hq, int32_t max_new,
@@ -192,7 +249,11 @@ q4gsw_status q4gsw_kv_attention_workspace_bytes(const q4gsw_kv_cache* c, int32_t
     q4gsw_status st = check_cache_shape(c);
     if (st != Q4GSW_OK) return st;
     if ((st = check_attention(c, batch, tokens, hq, max_new, max_ctx)) != Q4GSW_OK) return st;
-    *bytes = plan_attention(c->heads, c->dim, batch, tokens, hq, max_new, max_ctx, 0).ws_bytes;
+    // a window changes the span of keys, with which either plan's splits grow, and may change the plan
+    const AttnSize n = attention_size(c->heads, c->dim, batch, hq, max_new, max_ctx, 0, kBF16);
+    const uint64_t few = plan_workspace(plan_rows(n), tokens, hq, c->dim);
+    const uint64_t many = n.rows <= 32 ? 0 : plan_workspace(plan_prompt(n), tokens, hq, c->dim);
+    *bytes = few > many ? few : many;
     return Q4GSW_OK;
 }
 
@@ -213,11 +274,12 @@ q4gsw_status q4gsw_kv_attention(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s,
     const int es = esize(dtype);
     if (q_ld < row || q_ld > kMaxDim) return Q4GSW_E_SHAPE;
     if (!aligned16(q) || !aligned16(out) || (q_ld * es) % 16 != 0) return Q4GSW_E_ALIGN;
-    const AttnPlan p = plan_attention(c->heads, c->dim, s->batch, s->tokens, hq, max_new, max_ctx, window);
+    const AttnPlan p = plan_attention(attention_size(c->heads, c->dim, s->batch, hq, max_new, max_ctx, window, dtype));
+    const uint64_t need = plan_workspace(p, s->tokens, hq, c->dim);
     if ((int64_t)p.splits * p.row_tiles > kMaxBlocks / ((int64_t)s->batch * c->heads)) return Q4GSW_E_SHAPE;
-    if (!ws_ok(ws, ws_bytes, p.ws_bytes)) return Q4GSW_E_WORKSPACE;
+    if (!ws_ok(ws, ws_bytes, need)) return Q4GSW_E_WORKSPACE;
     const Range qr = range_of(q, rows_extent(s->tokens, q_ld, row, es));
-    const Range orr = range_of(out, (uint64_t)s->tokens * row * es), sr = range_of(ws, p.ws_bytes);
+    const Range orr = range_of(out, (uint64_t)s->tokens * row * es), sr = range_of(ws, need);
     if (overlap(orr, qr) || overlap(orr, cr) || overlap(sr, orr) || overlap(sr, qr) || overlap(sr, cr))
         return Q4GSW_E_ALIAS;
     a.q = q;
@@ -237,7 +299,7 @@ q4gsw_status q4gsw_kv_attention(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s,
     a.chunk = p.chunk;
     a.row_tiles = p.row_tiles;
     hipStream_t st_ = static_cast<hipStream_t>(stream);
-    hipError_t e = p.prompt ? launch_kv_prompt(a, p.waves, st_) : launch_kv_rows(a, p.r, p.waves, st_);
+    hipError_t e = p.prompt ? launch_kv_prompt(a, p.waves, st_) : launch_kv_rows(a, p.waves, st_);
     if (e == hipSuccess && p.splits > 1) e = launch_kv_join(a, st_);
     return hip_status(e);
 }
