@@ -58,17 +58,16 @@ struct KvSeq {
 };
 
 // The sequence's numbers with every row inside [0, tokens] and every length at least 0.
-__device__ __forceinline__ KvSeq kv_seq(const KvSeqs& s, int b) {
+__device__ __forceinline__ KvSeq kv_seq(int64_t tokens, int64_t lo, int64_t hi, int len) {
     KvSeq r;
-    int64_t lo = s.cu[b], hi = s.cu[b + 1];
-    lo = lo < 0 ? 0 : (lo > s.tokens ? s.tokens : lo);
-    hi = hi < lo ? lo : (hi > s.tokens ? s.tokens : hi);
+    lo = lo < 0 ? 0 : (lo > tokens ? tokens : lo);
+    hi = hi < lo ? lo : (hi > tokens ? tokens : hi);
     r.first_row = lo;
     r.m = (int)(hi - lo);
-    const int len = s.lens[b];
     r.len = len < 0 ? 0 : len;
     return r;
 }
+__device__ __forceinline__ KvSeq kv_seq(const KvSeqs& s, int b) { return kv_seq(s.tokens, s.cu[b], s.cu[b + 1], s.lens[b]); }
 
 // Byte offset of word w of `lane` in a code plane.
 template <int G>

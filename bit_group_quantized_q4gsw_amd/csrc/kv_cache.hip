@@ -24,23 +24,34 @@ constexpr int kThreads = 256;
 struct BlockAt {
     int t0, t1;          // the block's new tokens: places [t0, t1); none if t0 >= t1
     int64_t row0;        // token row of place 0 (may lie before the sequence's first)
-    uint8_t* unit;       // null: no page of the cache holds the block
+    int page, sub;       // its page (negative or past the cache: none holds the block) and block of the page
+    __device__ __forceinline__ uint8_t* unit(const KvView& c, int head) const {
+        return page >= 0 && page < c.pages ? c.data + kv_unit(c, page, head, sub) : nullptr;
+    }
 };
 
 // The block that workgroup `w` serves.  Places before 0 (more new tokens than the length) count on
-// downwards, so that every row of a sequence belongs to one workgroup.
-__device__ __forceinline__ BlockAt find_block(const KvView& c, const KvSeqs& sq, int64_t w, int head) {
-    BlockAt r{0, 0, 0, nullptr};
+// downwards, so that every row of a sequence belongs to one workgroup.  A batch of up to 64 takes one
+// round of loads for its sequence and one for its page, which nothing here waits for.
+__device__ __forceinline__ BlockAt find_block(const KvView& c, const KvSeqs& sq, int64_t w) {
+    BlockAt r{0, 0, 0, -1, 0};
     const int lane = threadIdx.x & 63;
-    int count = 0;
+    int count = 0, lo = 0, hi = 0, len = 0;
     for (int b0 = 0; b0 < sq.batch; b0 += 64) {
-        const int b = b0 + lane;
-        const bool before = b < sq.batch && (int64_t)(max(sq.cu[min(b, sq.batch - 1)], 0) >> 5) + 2 * (int64_t)b <= w;
+        const int b = min(b0 + lane, sq.batch - 1);
+        lo = sq.cu[b];
+        hi = sq.cu[b + 1];
+        len = sq.lens[b];
+        const bool before = b0 + lane < sq.batch && (int64_t)(max(lo, 0) >> 5) + 2 * (int64_t)b <= w;
         count += __popcll(__ballot(before));
     }
     if (count == 0) return r;
     const int b = __builtin_amdgcn_readfirstlane(min(count, sq.batch) - 1);
-    const KvSeq s = kv_seq(sq, b);
+    KvSeq s;
+    if (sq.batch <= 64)
+        s = kv_seq(sq.tokens, __builtin_amdgcn_readlane(lo, b), __builtin_amdgcn_readlane(hi, b), __builtin_amdgcn_readlane(len, b));
+    else
+        s = kv_seq(sq, b);
     const int64_t k = w - ((s.first_row >> 5) + 2 * (int64_t)b);
     const int64_t p0 = (int64_t)s.len - s.m;            // place of the first new token
     const int64_t blk = (p0 >> 5) + k;
@@ -50,30 +61,36 @@ __device__ __forceinline__ BlockAt find_block(const KvView& c, const KvSeqs& sq,
     r.row0 = s.first_row + 32 * blk - p0;
     const int64_t at = blk >> c.bpp_log2;
     if (blk < 0 || at >= sq.table_cols) return r;
-    const int64_t page = sq.table[(int64_t)b * sq.table_ld + at];
-    if (page >= 0 && page < c.pages) r.unit = c.data + kv_unit(c, page, head, (int)(blk & ((1 << c.bpp_log2) - 1)));
+    r.page = sq.table[(int64_t)b * sq.table_ld + at];
+    r.sub = (int)(blk & ((1 << c.bpp_log2) - 1));
     return r;
 }
 
-// 8 elements at e (a multiple of 8; the base is 16-byte aligned) as fp32
+// 8 elements as they lie in memory, from a 16-byte aligned place, and as fp32
 template <int XT>
-__device__ __forceinline__ void load8(const void* x, int64_t e, float (&v)[8]) {
-    if constexpr (XT == kF32) {
-        const f4 a = bitcast<f4>(ldg16(static_cast<const float*>(x) + e));
-        const f4 b = bitcast<f4>(ldg16(static_cast<const float*>(x) + e + 4));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-    } else {
-        const u4 a = ldg16(static_cast<const uint16_t*>(x) + e);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = XT == kF16 ? f16_bits_to_f32((uint16_t)(a[i] & 0xFFFFu)) : bitcast<float>(a[i] << 16);
-            v[2 * i + 1] = XT == kF16 ? f16_bits_to_f32((uint16_t)(a[i] >> 16)) : bitcast<float>(a[i] & 0xFFFF0000u);
+struct Raw8 {
+    u4 w[XT == kF32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* x, int64_t e) {
+        if constexpr (XT == kF32) {
+            w[0] = ldg16(static_cast<const float*>(x) + e);
+            w[1] = ldg16(static_cast<const float*>(x) + e + 4);
+        } else {
+            w[0] = ldg16(static_cast<const uint16_t*>(x) + e);
         }
     }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (XT == kF32) return bitcast<float>(w[i >> 2][i & 3]);
+        const uint32_t h = w[0][i >> 1];
+        if constexpr (XT == kF16) return f16_bits_to_f32((uint16_t)((i & 1) ? h >> 16 : h & 0xFFFFu));
+        return bitcast<float>((i & 1) ? h & 0xFFFF0000u : h << 16);
+    }
+};
+
+// v as a whole number, saturated; NaN gives 0
+__device__ __forceinline__ int to_int(float v) {
+    int r;
+    asm("v_cvt_i32_f32 %0, %1" : "=v"(r) : "v"(v));
+    return r;
 }
 
 // Four lanes hold the 32 channels of a scale, 8 each.  The arithmetic follows the definition step
@@ -84,39 +101,46 @@ template <int XT, int D>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvView c, KvSeqs sq, const void* __restrict__ k, int64_t k_ld,
                                                              const void* __restrict__ v, int64_t v_ld) {
     constexpr int G = D / 32, kOct = D / 8, kItems = 32 * kOct;
+    // 24 bytes more a token: the four tokens that a wave gathers at once lie in other banks
+    constexpr int kVcRow = D + 24;
     __shared__ uint32_t s_kw[128 * G];                     // keys' words in plane order
-    __shared__ __attribute__((aligned(16))) uint8_t s_vc[32 * D];    // values' codes [token][channel]
+    __shared__ __attribute__((aligned(16))) uint8_t s_vc[32 * kVcRow];    // values' codes [token][channel]
     __shared__ uint16_t s_sc[2][32 * G];                   // scales in layout order
     const int tid = threadIdx.x, head = blockIdx.y;
-    const BlockAt at = find_block(c, sq, blockIdx.x, head);
-    uint8_t* unit = at.unit;
-    if (!unit || at.t0 >= at.t1) return;
+    const BlockAt at = find_block(c, sq, blockIdx.x);
+    if (at.t0 >= at.t1) return;
 
+    // every load of the thread before the first use of one
+    constexpr int kPer = (kItems + kThreads - 1) / kThreads;
+    Raw8<XT> raw[2][kPer];
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-        const void* src = kv ? v : k;
-        const int64_t ld = kv ? v_ld : k_ld;
-        for (int it = tid; it < kItems; it += kThreads) {
-            const int t = it / kOct, o = it - t * kOct, g = o >> 2;
-            if (t < at.t0 || t >= at.t1) continue;         // a group's four lanes stay together
-            float x[8];
-            load8<XT>(src, (at.row0 + t) * ld + head * D + 8 * o, x);
-            float amax = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] = x[e] == x[e] ? x[e] : 0.0f;
-                amax = fmaxf(amax, fabsf(x[e]));
-            }
+        for (int j = 0; j < kPer; ++j) {
+            const int it = tid + j * kThreads, t = it / kOct, o = it - t * kOct;
+            if (t >= at.t0 && t < at.t1) raw[kv][j].load(kv ? v : k, (at.row0 + t) * (kv ? v_ld : k_ld) + head * D + 8 * o);
+        }
+    }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int it = tid + j * kThreads, t = it / kOct, o = it - t * kOct, g = o >> 2;
+            if (t < at.t0 || t >= at.t1) continue;         // a group's four lanes stay together
+            const Raw8<XT>& x = raw[kv][j];
+            float amax = 0.0f;                             // fmaxf passes NaN over
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
             amax = fmaxf(amax, __shfl_xor(amax, 1));
             amax = fmaxf(amax, __shfl_xor(amax, 2));
             const _Float16 sh = (_Float16)fminf(amax / 7.0f, 8188.0f);
             const float s = (float)sh;
-            const float inv = 1.0f / s;
+            const float inv = s > 0.0f ? 1.0f / s : 0.0f;
             uint32_t code[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float r = s > 0.0f ? fminf(fmaxf(rintf(x[e] * inv), -8.0f), 7.0f) : 0.0f;
-                code[e] = (uint32_t)((int)r + 8);
+                const int r = to_int(rintf(x[e] * inv));
+                code[e] = (uint32_t)((r < -8 ? -8 : (r > 7 ? 7 : r)) + 8);
             }
             const int q = kv_q(t), slot = kv_slot(t);
             if (kv == 0) {
@@ -128,12 +152,14 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvView c, KvSeqs sq
                 u2 w = {0u, 0u};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e >> 2] |= code[e] << (8 * (e & 3));
-                *reinterpret_cast<u2*>(&s_vc[t * D + 8 * o]) = w;
+                *reinterpret_cast<u2*>(&s_vc[t * kVcRow + 8 * o]) = w;
             }
             if ((o & 3) == 0) s_sc[kv][(q * G + g) * 8 + slot] = bitcast<uint16_t>(sh);
         }
     }
     __syncthreads();
+    uint8_t* const unit = at.unit(c, head);
+    if (!unit) return;
 
     // words of one plane in address order: lane and word of 4-byte place n
     auto place = [](int n, int& w, int& lane) {
@@ -161,7 +187,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvView c, KvSeqs sq
         for (int slot = 0; slot < 8; ++slot) {
             const int tt = kv_tok(q, slot);
             if (tt < at.t0 || tt >= at.t1) continue;
-            word |= (uint32_t)s_vc[tt * D + 16 * w + i] << (4 * nib_pos(slot));
+            word |= (uint32_t)s_vc[tt * kVcRow + 16 * w + i] << (4 * nib_pos(slot));
             mask |= 0xFu << (4 * nib_pos(slot));
         }
         if (mask == 0xFFFFFFFFu) vw[n] = word;
@@ -182,11 +208,12 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvView c, KvSeqs sq, 
     constexpr int G = D / 32, kOct = D / 8;
     __shared__ __attribute__((aligned(16))) uint8_t s_unit[1152 * G];
     const int tid = threadIdx.x, head = blockIdx.y;
-    const BlockAt at = find_block(c, sq, blockIdx.x, head);
+    const BlockAt at = find_block(c, sq, blockIdx.x);
     if (at.t0 >= at.t1) return;
+    const uint8_t* const unit = at.unit(c, head);
     // a block without a page reads as a unit of zeros: scale 0
     for (int n = tid; n < 72 * G; n += kThreads)
-        *reinterpret_cast<u4*>(&s_unit[16 * n]) = at.unit ? ldg16(at.unit + 16 * n) : u4{0u, 0u, 0u, 0u};
+        *reinterpret_cast<u4*>(&s_unit[16 * n]) = unit ? ldg16(unit + 16 * n) : u4{0u, 0u, 0u, 0u};
     __syncthreads();
     const uint16_t* ksc = reinterpret_cast<const uint16_t*>(s_unit + 1024 * G);
     const uint16_t* vsc = ksc + 32 * G;
