@@ -23,6 +23,8 @@
 
 namespace q4gsw {
 
+typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+
 constexpr int kKvTok = 32;               // tokens of a block
 constexpr int kKvGroup = 32;             // channels of a scale
 constexpr int kKvMinPage = 32, kKvMaxPage = 4096;
