@@ -77,6 +77,19 @@ class KvSeqs(ctypes.Structure):
                 ("tokens", ctypes.c_int64)]
 
 
+class KvPlanInfo(ctypes.Structure):
+    """q4gsw_kv_plan_info of include/q4gsw.h."""
+    _fields_ = [("kernel", ctypes.c_int32), ("waves", ctypes.c_int32), ("splits", ctypes.c_int32)]
+
+
+class KvOptions(ctypes.Structure):
+    """q4gsw_kv_options of include/q4gsw.h."""
+    _fields_ = [("kernel", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+KV_KERNELS = {"any": 0, "few_rows": 1, "many_rows": 2}
+
+
 # Choices made by forced_route / forced_plan, held per Python thread and handed to each call
 # (the library itself keeps no routing state).
 _local = threading.local()
@@ -104,6 +117,7 @@ def lib() -> ctypes.CDLL:
         i32, i64, u64, vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
         pw = ctypes.POINTER(WeightDesc)
         po = ctypes.POINTER(Options)
+        ko = ctypes.POINTER(KvOptions)
         pc, ps = ctypes.POINTER(KvCacheDesc), vp       # sequences: a KvSeqs by reference or its packed bytes
         sigs = {
             "q4gsw_packed_bytes": [i64, i64, i64, i32, ctypes.POINTER(u64)],
@@ -134,7 +148,9 @@ def lib() -> ctypes.CDLL:
             "q4gsw_kv_append": [pc, ps, vp, i64, vp, i64, i32, vp],
             "q4gsw_kv_read": [pc, ps, vp, vp, vp],
             "q4gsw_kv_attention_workspace_bytes": [pc, i32, i64, i32, i32, i32, ctypes.POINTER(u64)],
+            "q4gsw_kv_attention_plan": [pc, i32, i64, i32, i32, i32, i32, i32, ko, ctypes.POINTER(KvPlanInfo)],
             "q4gsw_kv_attention": [pc, ps, vp, i64, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, u64, vp],
+            "q4gsw_kv_attention_ex": [pc, ps, vp, i64, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, u64, ko, vp],
             "q4gsw_adapter_workspace_bytes": [i32, pw, i64, i32, i32, ctypes.POINTER(u64)],
             "q4gsw_adapter_fwd": [pw, vp, i32, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, u64, vp],
             "q4gsw_adapter_bwd": [pw, vp, vp, i32, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, vp, vp, u64, vp],
@@ -533,6 +549,16 @@ def kv_attention_workspace_bytes(cache: KvCache, batch: int, tokens: int, hq: in
     return out.value
 
 
+def kv_attention_plan(cache: KvCache, batch: int, tokens: int, hq: int, max_new: int, max_ctx: int,
+                      dtype: torch.dtype, window: int = 0) -> dict:
+    """How a kv_attention call with these sizes runs: the kernel ("few_rows" or "many_rows"), waves
+    per workgroup and splits of the cache's length."""
+    info = KvPlanInfo()
+    _check(lib().q4gsw_kv_attention_plan(cache._ref, batch, tokens, hq, max_new, max_ctx, window, _TORCH_DTYPE[dtype],
+                                         getattr(_local, "kv", None), ctypes.byref(info)), "q4gsw_kv_attention_plan")
+    return {"kernel": next(k for k, v in KV_KERNELS.items() if v == info.kernel), "waves": info.waves, "splits": info.splits}
+
+
 def kv_attention(cache: KvCache, q: torch.Tensor, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor,
                  max_new: int, max_ctx: int, window: int = 0, softcap: float = 0.0,
                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -555,9 +581,9 @@ def kv_attention(cache: KvCache, q: torch.Tensor, table: torch.Tensor, cu: torch
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != cache._dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {cache.buffer.device}")
-    _check(lib().q4gsw_kv_attention(cache._ref, seqs, qp, q_ld, _TORCH_DTYPE[dt], hq, max_new, max_ctx, window, softcap,
-                                    out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream()),
-           "q4gsw_kv_attention")
+    _check(lib().q4gsw_kv_attention_ex(cache._ref, seqs, qp, q_ld, _TORCH_DTYPE[dt], hq, max_new, max_ctx, window,
+                                       softcap, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                       getattr(_local, "kv", None), _stream()), "q4gsw_kv_attention")
     return out
 
 
@@ -732,6 +758,18 @@ def forced_route(name: str):
     benchmarks); a call the family cannot serve raises Q4gswError with E_ROUTE."""
     with _with_options(route=ROUTES[name]):
         yield
+
+
+@contextlib.contextmanager
+def forced_kv_kernel(name: str):
+    """Send the kv_attention calls made by this thread inside the block to one kernel, "few_rows" or
+    "many_rows" (tests and benchmarks); Q4gswError with E_ROUTE where it cannot serve a call."""
+    old = getattr(_local, "kv", None)
+    _local.kv = ctypes.pointer(KvOptions(KV_KERNELS[name], 0))
+    try:
+        yield
+    finally:
+        _local.kv = old
 
 
 def build_info() -> str:

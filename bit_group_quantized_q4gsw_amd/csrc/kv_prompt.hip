@@ -13,8 +13,10 @@
 // output's, since scores feel it; with PREC (fp16 and fp32 outputs) the exact remainder of every
 // key and value is kept beside it and enters by a second product.
 //
-// Bound: MFMA and the softmax's VALU, about even at 128 channels: a 32x32 tile of scores takes 16
-// products of 32 cycles (32 with PREC) and 16 times some 30 cycles of VALU.
+// Bound: MFMA and the softmax's VALU, about even at 128 channels (a wave's turn of 64 keys: 32 products of
+// 32 cycles, some 230 VALU of 4 and more) and hardly overlapping between the two waves of a SIMD:
+// three chunks of 2048 rows behind 6144 keys, 32 / 8 heads of 128, run at 940 TFLOP/s (a large
+// library product: 1206), unlike ones (1024 .. 2048 rows of 8192 and fewer) at 850 to 890.
 #include "kv_attention.h"
 
 namespace q4gsw {

@@ -14,7 +14,8 @@
 // order 0, 4, 1, 5, 2, 6, 3, 7, padding 0, minus the zero point), so linears of the same rows
 // start at once; optionally the values scale * (code - zero) go out as fp32 too.
 //
-// Bound: HBM.
+// Bound: HBM: 4096 rows of 8192, bf16, with h and values written, 369 MB in 82 us, 4.5 TB/s (a large
+// copy: 4.72); 4 rows of 2048 take 3.1 us, two rounds of loads and one join.
 #include "device.h"
 #include "internal.h"
 

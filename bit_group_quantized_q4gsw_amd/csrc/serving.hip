@@ -80,6 +80,7 @@ struct AttnSize {
 };
 
 constexpr int kCus = 256;
+constexpr int kFewRows = 32;     // never the kernel of many rows
 
 void finish_plan(AttnPlan& p, const AttnSize& n, int64_t splits) {
     p.splits = (int)(splits < 1 ? 1 : splits);
@@ -150,9 +151,10 @@ AttnSize attention_size(int heads, int dim, int batch, int hq, int max_new, int 
 // against many rows: 512 tokens 18 against 23 us, 1024 tokens 40 against 56, 2048 tokens 111 against
 // 127, two of 2048 tokens 203 against 94; 1024 tokens behind 7000: 367 against 185).  Up to 32 rows
 // never fill the workgroup of many.
-AttnPlan plan_attention(const AttnSize& n) {
+AttnPlan plan_attention(const AttnSize& n, int kernel) {
+    if (kernel == Q4GSW_KV_MANY_ROWS) return plan_prompt(n);
     const AttnPlan few = plan_rows(n);
-    if (n.rows <= 32) return few;
+    if (n.rows <= kFewRows || kernel == Q4GSW_KV_FEW_ROWS) return few;
     const AttnPlan many = plan_prompt(n);
     return many.us < few.us ? many : few;
 }
@@ -167,6 +169,15 @@ q4gsw_status check_attention(const q4gsw_kv_cache* c, int64_t batch, int64_t tok
         hq % c->heads != 0 || max_new < 1 || max_new > kMaxM || max_ctx < 0)
         return Q4GSW_E_SHAPE;
     if (tokens * hq > kMaxBlocks || (int64_t)max_new * (hq / c->heads) > kMaxBlocks / 2) return Q4GSW_E_SHAPE;
+    return Q4GSW_OK;
+}
+
+q4gsw_status read_kernel(const q4gsw_kv_options* o, const q4gsw_kv_cache* c, int32_t hq, int32_t max_new, int* kernel) {
+    *kernel = o ? o->kernel : Q4GSW_KV_ANY;
+    if (!o) return Q4GSW_OK;
+    if (o->reserved != 0) return Q4GSW_E_SHAPE;
+    if (*kernel < Q4GSW_KV_ANY || *kernel > Q4GSW_KV_MANY_ROWS) return Q4GSW_E_ROUTE;
+    if (*kernel == Q4GSW_KV_MANY_ROWS && (int64_t)max_new * (hq / c->heads) <= kFewRows) return Q4GSW_E_ROUTE;
     return Q4GSW_OK;
 }
 
@@ -252,14 +263,38 @@ q4gsw_status q4gsw_kv_attention_workspace_bytes(const q4gsw_kv_cache* c, int32_t
     // a window changes the span of keys, with which either plan's splits grow, and may change the plan
     const AttnSize n = attention_size(c->heads, c->dim, batch, hq, max_new, max_ctx, 0, kBF16);
     const uint64_t few = plan_workspace(plan_rows(n), tokens, hq, c->dim);
-    const uint64_t many = n.rows <= 32 ? 0 : plan_workspace(plan_prompt(n), tokens, hq, c->dim);
+    const uint64_t many = n.rows <= kFewRows ? 0 : plan_workspace(plan_prompt(n), tokens, hq, c->dim);
     *bytes = few > many ? few : many;
+    return Q4GSW_OK;
+}
+
+q4gsw_status q4gsw_kv_attention_plan(const q4gsw_kv_cache* c, int32_t batch, int64_t tokens, int32_t hq, int32_t max_new,
+                                     int32_t max_ctx, int32_t window, int32_t dtype, const q4gsw_kv_options* opts,
+                                     q4gsw_kv_plan_info* info) {
+    if (!info) return Q4GSW_E_NULL;
+    q4gsw_status st = check_cache_shape(c);
+    if (st != Q4GSW_OK) return st;
+    if ((st = check_attention(c, batch, tokens, hq, max_new, max_ctx)) != Q4GSW_OK) return st;
+    if (window < 0) return Q4GSW_E_SHAPE;
+    if (!act_dtype_ok(dtype)) return Q4GSW_E_DTYPE;
+    int kernel = 0;
+    if ((st = read_kernel(opts, c, hq, max_new, &kernel)) != Q4GSW_OK) return st;
+    const AttnPlan p = plan_attention(attention_size(c->heads, c->dim, batch, hq, max_new, max_ctx, window, dtype), kernel);
+    *info = q4gsw_kv_plan_info{p.prompt ? Q4GSW_KV_MANY_ROWS : Q4GSW_KV_FEW_ROWS, p.waves, p.splits};
     return Q4GSW_OK;
 }
 
 q4gsw_status q4gsw_kv_attention(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s, const void* q, int64_t q_ld,
                                 int32_t dtype, int32_t hq, int32_t max_new, int32_t max_ctx, int32_t window,
                                 float softcap, void* out, void* ws, uint64_t ws_bytes, void* stream) {
+    return q4gsw_kv_attention_ex(c, s, q, q_ld, dtype, hq, max_new, max_ctx, window, softcap, out, ws, ws_bytes, nullptr,
+                                 stream);
+}
+
+q4gsw_status q4gsw_kv_attention_ex(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s, const void* q, int64_t q_ld,
+                                   int32_t dtype, int32_t hq, int32_t max_new, int32_t max_ctx, int32_t window,
+                                   float softcap, void* out, void* ws, uint64_t ws_bytes, const q4gsw_kv_options* opts,
+                                   void* stream) {
     KvAttnArgs a{};
     Range cr;
     q4gsw_status st = check_cache(c, &a.c, &cr);
@@ -268,13 +303,16 @@ q4gsw_status q4gsw_kv_attention(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s,
     if ((st = check_attention(c, s->batch, s->tokens, hq, max_new, max_ctx)) != Q4GSW_OK) return st;
     if (window < 0 || !(softcap == 0.0f || (softcap >= kMinCap && softcap <= kMaxCap))) return Q4GSW_E_SHAPE;
     if (!act_dtype_ok(dtype)) return Q4GSW_E_DTYPE;
+    int kernel = 0;
+    if ((st = read_kernel(opts, c, hq, max_new, &kernel)) != Q4GSW_OK) return st;
     if (s->tokens == 0) return Q4GSW_OK;
     if (!q || !out) return Q4GSW_E_NULL;
     const int64_t row = (int64_t)hq * c->dim;
     const int es = esize(dtype);
     if (q_ld < row || q_ld > kMaxDim) return Q4GSW_E_SHAPE;
     if (!aligned16(q) || !aligned16(out) || (q_ld * es) % 16 != 0) return Q4GSW_E_ALIGN;
-    const AttnPlan p = plan_attention(attention_size(c->heads, c->dim, s->batch, hq, max_new, max_ctx, window, dtype));
+    const AttnPlan p = plan_attention(attention_size(c->heads, c->dim, s->batch, hq, max_new, max_ctx, window, dtype),
+                                      kernel);
     const uint64_t need = plan_workspace(p, s->tokens, hq, c->dim);
     if ((int64_t)p.splits * p.row_tiles > kMaxBlocks / ((int64_t)s->batch * c->heads)) return Q4GSW_E_SHAPE;
     if (!ws_ok(ws, ws_bytes, need)) return Q4GSW_E_WORKSPACE;

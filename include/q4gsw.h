@@ -468,7 +468,8 @@ q4gsw_status q4gsw_kv_read(const q4gsw_kv_cache *c, const q4gsw_kv_seqs *s, floa
  *   ws   device workspace of ws_bytes >= q4gsw_kv_attention_workspace_bytes (256-byte aligned; may be
  *        NULL when that is 0)
  * Scores, the softmax and all sums are held in fp32; keys, values and weights enter the products as
- * fp16 (one rounding each).  Results do not depend on the launch.  Tokens of 0 launch nothing.
+ * fp16 (one rounding each).  A call's results repeat bit for bit; other bounds max_new and max_ctx may
+ * order its sums otherwise.  Tokens of 0 launch nothing.
  * E_NULL, E_SHAPE (hq not a multiple of heads; sizes; window negative; softcap neither 0 nor in 1e-30..1e30),
  * E_DTYPE, E_BUFFER, E_ALIGN, E_WORKSPACE, E_ALIAS (out or ws overlaps q, the cache or each other).
  */
@@ -477,6 +478,33 @@ q4gsw_status q4gsw_kv_attention_workspace_bytes(const q4gsw_kv_cache *c, int32_t
 q4gsw_status q4gsw_kv_attention(const q4gsw_kv_cache *c, const q4gsw_kv_seqs *s, const void *q, int64_t q_ld,
                                 int32_t dtype, int32_t hq, int32_t max_new, int32_t max_ctx, int32_t window,
                                 float softcap, void *out, void *ws, uint64_t ws_bytes, void *stream);
+
+/* Per-call choice of the kernel, for tests and benchmarks (opts NULL: none; E_ROUTE: unknown kernel, or
+ * the one of many rows where max_new * hq / heads is 32 or less). */
+typedef enum q4gsw_kv_kernel {
+    Q4GSW_KV_ANY = 0,
+    Q4GSW_KV_FEW_ROWS = 1,    /* a wave per 32-token unit, tiles of 16 rows */
+    Q4GSW_KV_MANY_ROWS = 2    /* 32 rows a wave, tiles of keys shared by the workgroup */
+} q4gsw_kv_kernel;
+typedef struct q4gsw_kv_options {
+    int32_t kernel;           /* q4gsw_kv_kernel */
+    int32_t reserved;         /* 0 */
+} q4gsw_kv_options;
+q4gsw_status q4gsw_kv_attention_ex(const q4gsw_kv_cache *c, const q4gsw_kv_seqs *s, const void *q, int64_t q_ld,
+                                   int32_t dtype, int32_t hq, int32_t max_new, int32_t max_ctx, int32_t window,
+                                   float softcap, void *out, void *ws, uint64_t ws_bytes,
+                                   const q4gsw_kv_options *opts, void *stream);
+
+/* Plan attestation for tests and benchmarks: how kv_attention with these arguments runs.  Host only.
+ * E_NULL, E_SHAPE, E_DTYPE, E_ROUTE. */
+typedef struct q4gsw_kv_plan_info {
+    int32_t kernel;           /* Q4GSW_KV_FEW_ROWS or Q4GSW_KV_MANY_ROWS */
+    int32_t waves;            /* per workgroup */
+    int32_t splits;           /* of the cache's length (more than one: a second launch joins them) */
+} q4gsw_kv_plan_info;
+q4gsw_status q4gsw_kv_attention_plan(const q4gsw_kv_cache *c, int32_t batch, int64_t tokens, int32_t hq,
+                                     int32_t max_new, int32_t max_ctx, int32_t window, int32_t dtype,
+                                     const q4gsw_kv_options *opts, q4gsw_kv_plan_info *info);
 
 /* Route attestation: the q4gsw_route_id a plain call (no options) with these
  * arguments takes (Q4GSW_ROUTE_NONE if it would fail validation).  For
