@@ -92,12 +92,17 @@ KV_KERNELS = {"any": 0, "few_rows": 1, "many_rows": 2}
 
 # Choices made by forced_route / forced_plan, held per Python thread and handed to each call
 # (the library itself keeps no routing state).
-_local = threading.local()
+class _Local(threading.local):
+    opts = None
+    kv = None
+
+
+_local = _Local()
 
 
 def _opts():
     """The current thread's options, or None (library defaults)."""
-    o = getattr(_local, "opts", None)
+    o = _local.opts
     if o is None or (o.route == 0 and o.tile_rows == 0 and o.splits == 0):
         return None
     return ctypes.byref(o)
@@ -496,36 +501,36 @@ def _kv_seqs(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, lens: torch.
     return _pack_seqs(table.data_ptr(), ld, cols, B, cu.data_ptr(), lens.data_ptr(), tokens)
 
 
-def _token_rows(t: torch.Tensor, heads: int, cache: KvCache, name: str) -> Tuple[torch.Tensor, int, int]:
-    """(tensor, its address, token pitch in elements): `t` itself where its token rows are dense and
-    16-byte aligned (a slice of a fused projection's output, say), else a copy."""
+def _token_rows(t: torch.Tensor, heads: int, cache: KvCache, name: str) -> Tuple[torch.Tensor, int, int, int]:
+    """(tensor, its address, token pitch in elements, dtype code): `t` itself where its token rows are
+    dense and 16-byte aligned (a slice of a fused projection's output, say), else a copy."""
     dim = cache.dim
+    code = _TORCH_DTYPE.get(t.dtype)
     n, th, td = t.shape if t.dim() == 3 else (0, 0, 0)
-    if th != heads or td != dim or t.get_device() != cache._dev or t.dtype not in _TORCH_DTYPE:
+    if th != heads or td != dim or code is None or t.get_device() != cache._dev:
         raise ValueError(f"{name} must be a floating tensor [tokens, {heads}, {dim}] on {cache.buffer.device}")
     ld, sh, sd = t.stride()
     row = heads * dim
     if n <= 1:
         ld = row
     ptr = t.data_ptr()
-    if sd != 1 or (sh != dim and heads > 1) or ld < row or (ptr | ld * t.element_size()) & 15:
+    if sd != 1 or (sh != dim and heads > 1) or ld < row or (ptr | ld * (4 if code == F32 else 2)) & 15:
         t = t.clone(memory_format=torch.contiguous_format)
-        return t, t.data_ptr(), row
-    return t, ptr, ld
+        return t, t.data_ptr(), row, code
+    return t, ptr, ld, code
 
 
 def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, cu: torch.Tensor,
               lens: torch.Tensor) -> None:
     """Store the keys and values k, v [tokens, heads, dim] of new tokens: rows cu[b] .. cu[b + 1] - 1
     are the last of sequence b's lens[b] tokens (with them), whose pages are table[b]."""
-    k, kp, k_ld = _token_rows(k, cache.heads, cache, "k")
-    v, vp, v_ld = _token_rows(v, cache.heads, cache, "v")
-    dt = k.dtype
+    k, kp, k_ld, dt = _token_rows(k, cache.heads, cache, "k")
+    v, vp, v_ld, v_dt = _token_rows(v, cache.heads, cache, "v")
     tokens = k.shape[0]
-    if v.dtype is not dt or v.shape[0] != tokens:
+    if v_dt != dt or v.shape[0] != tokens:
         raise ValueError("k and v must have one dtype and one number of tokens")
-    _check(lib().q4gsw_kv_append(cache._ref, _kv_seqs(cache, table, cu, lens, tokens), kp, k_ld, vp, v_ld,
-                                 _TORCH_DTYPE[dt], _stream()), "q4gsw_kv_append")
+    _check(lib().q4gsw_kv_append(cache._ref, _kv_seqs(cache, table, cu, lens, tokens), kp, k_ld, vp, v_ld, dt,
+                                 _stream()), "q4gsw_kv_append")
 
 
 def kv_read(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, tokens: int,
@@ -555,7 +560,7 @@ def kv_attention_plan(cache: KvCache, batch: int, tokens: int, hq: int, max_new:
     per workgroup and splits of the cache's length."""
     info = KvPlanInfo()
     _check(lib().q4gsw_kv_attention_plan(cache._ref, batch, tokens, hq, max_new, max_ctx, window, _TORCH_DTYPE[dtype],
-                                         getattr(_local, "kv", None), ctypes.byref(info)), "q4gsw_kv_attention_plan")
+                                         _local.kv, ctypes.byref(info)), "q4gsw_kv_attention_plan")
     return {"kernel": next(k for k, v in KV_KERNELS.items() if v == info.kernel), "waves": info.waves, "splits": info.splits}
 
 
@@ -570,7 +575,7 @@ def kv_attention(cache: KvCache, q: torch.Tensor, table: torch.Tensor, cu: torch
     shape = q.shape
     tokens, hq, _ = shape
     dt = q.dtype
-    q, qp, q_ld = _token_rows(q, hq, cache, "q")
+    q, qp, q_ld, code = _token_rows(q, hq, cache, "q")
     if out is None:
         out = torch.empty(shape, dtype=dt, device=q.device)
     elif out.dtype is not dt or out.shape != shape or out.get_device() != cache._dev or not out.is_contiguous():
@@ -581,9 +586,9 @@ def kv_attention(cache: KvCache, q: torch.Tensor, table: torch.Tensor, cu: torch
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != cache._dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {cache.buffer.device}")
-    _check(lib().q4gsw_kv_attention_ex(cache._ref, seqs, qp, q_ld, _TORCH_DTYPE[dt], hq, max_new, max_ctx, window,
-                                       softcap, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                       getattr(_local, "kv", None), _stream()), "q4gsw_kv_attention")
+    _check(lib().q4gsw_kv_attention_ex(cache._ref, seqs, qp, q_ld, code, hq, max_new, max_ctx, window, softcap,
+                                       out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                       _local.kv, _stream()), "q4gsw_kv_attention")
     return out
 
 
@@ -728,7 +733,7 @@ def plan(op: int, w: PackedWeight, M: int, dtype: torch.dtype, wk: PackedWeight 
 @contextlib.contextmanager
 def _with_options(**fields):
     """Set fields of this thread's per-call options for the calls inside the block."""
-    old = getattr(_local, "opts", None)
+    old = _local.opts
     new = Options()
     if old is not None:
         ctypes.memmove(ctypes.byref(new), ctypes.byref(old), ctypes.sizeof(Options))
@@ -764,7 +769,7 @@ def forced_route(name: str):
 def forced_kv_kernel(name: str):
     """Send the kv_attention calls made by this thread inside the block to one kernel, "few_rows" or
     "many_rows" (tests and benchmarks); Q4gswError with E_ROUTE where it cannot serve a call."""
-    old = getattr(_local, "kv", None)
+    old = _local.kv
     _local.kv = ctypes.pointer(KvOptions(KV_KERNELS[name], 0))
     try:
         yield

@@ -149,7 +149,7 @@ struct QueryRow {
     }
 };
 
-// Waves a SIMD holds of the kernel of few rows: what its registers allow (97, 134, 160, 200 and 256
+// Waves a SIMD holds of the kernel of few rows: what its registers allow (97, 134, 164, 202 and 256
 // for 64 .. 256 channels: sums D / 4, queries D / 8, and their starts).
 constexpr int kv_rows_waves(int D) { return D == 64 ? 4 : (D <= 128 ? 3 : 2); }
 

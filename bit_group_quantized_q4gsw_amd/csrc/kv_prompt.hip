@@ -11,7 +11,9 @@
 //   * sums: values as the first operand, 32 channels of a row in a lane's 16 accumulators.
 // Rounding code * scale to fp16 (2^-11) is below a bf16 output's own rounding but twice an fp16
 // output's, since scores feel it; with PREC (fp16 and fp32 outputs) the exact remainder of every
-// key and value is kept beside it and enters by a second product.
+// key and value is kept beside it and enters by a second product: rms error 2.2e-4 .. 2.8e-4, where
+// values without theirs give 2.8e-4 .. 3.4e-4 in 992 instead of 1255 us (three chunks of 2048 rows
+// behind 6144 keys, 32 / 8 heads of 128).
 //
 // Bound: MFMA and the softmax's VALU, about even at 128 channels (a wave's turn of 64 keys: 32 products of
 // 32 cycles, some 230 VALU of 4 and more) and hardly overlapping between the two waves of a SIMD:

@@ -163,7 +163,7 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
         sc[0] = sc[1] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if (g && (g & 1) == 0 && D >= 128) __builtin_amdgcn_sched_barrier(0);
+            if (g && (g & 3) == 0 && D >= 256) __builtin_amdgcn_sched_barrier(0);
             const u2 kw = word_pair<G>(unit, g, lane);
             const u4 ks = *reinterpret_cast<const u4*>(unit + 1024 * G + (qd * G + g) * 16);
             const float c0 = kBiased ? cb[g] : 0.0f;
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
         l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if (g && (g & 1) == 0 && D >= 128) __builtin_amdgcn_sched_barrier(0);
+            if (g && (g & 3) == 0 && D >= 256) __builtin_amdgcn_sched_barrier(0);
             const u2 vw = word_pair<G>(unit + 512 * G, g, lane);
             const u4 vs = scales(g);
             u4 pw;
@@ -318,9 +318,12 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
 // out[row] = sum_s 2^(m_s - m) part_s / sum_s 2^(m_s - m) l_s: a thread takes every kPar-th split,
 // kBatch of them in flight, on a running reference of its own, and the threads of a channel join in
 // a fixed order.  A split that saw no key (l 0) wrote no sums: what stands there is loaded but not used.
-template <int D>
-__global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs a) {
-    constexpr int kQuads = D / 4, kPar = 256 / kQuads, kBatch = 4;
+constexpr int kJoinBatch = 4;
+constexpr int join_splits(int D, int threads) { return kJoinBatch * (threads / (D / 4)); }   // in one round
+
+template <int D, int THREADS>
+__global__ __launch_bounds__(THREADS) void kv_join_kernel(KvAttnArgs a) {
+    constexpr int kQuads = D / 4, kPar = THREADS / kQuads, kBatch = kJoinBatch;
     __shared__ __attribute__((aligned(16))) f4 s_acc[kPar * kQuads];
     __shared__ float s_l[kPar], s_m[kPar];
     const int tid = threadIdx.x;
@@ -399,9 +402,13 @@ hipError_t launch_kv_rows(const KvAttnArgs& a, int waves, hipStream_t s) {
 }
 
 hipError_t launch_kv_join(const KvAttnArgs& a, hipStream_t s) {
+    // one wave a row where it takes the splits in one round
     const dim3 grid((unsigned)(a.sq.tokens * a.hq));
-#define Q4GSW_KV_JOIN(D) \
-    case D: hipLaunchKernelGGL((kv_join_kernel<D>), grid, dim3(256), 0, s, a); break;
+#define Q4GSW_KV_JOIN(D)                                                                                                  \
+    case D:                                                                                                               \
+        if (a.splits <= join_splits(D, 64)) hipLaunchKernelGGL((kv_join_kernel<D, 64>), grid, dim3(64), 0, s, a);           \
+        else hipLaunchKernelGGL((kv_join_kernel<D, 256>), grid, dim3(256), 0, s, a);                                        \
+        break;
     switch (a.c.dim) {
         Q4GSW_KV_JOIN(64)
         Q4GSW_KV_JOIN(96)

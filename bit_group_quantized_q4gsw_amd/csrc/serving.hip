@@ -96,7 +96,7 @@ void finish_plan(AttnPlan& p, const AttnSize& n, int64_t splits) {
 // launch costs more (509 tokens, heads of 64: 6.6 us, 2 splits 8.5; four of 1024, heads of 128: 10.9 us,
 // 4 splits 9.4).  Where that leaves long
 // splits and few turns, unlike lengths end at unlike times, and shorter splits balance them (64
-// sequences of 4096 .. 16384: 1 split 209 us, 8 splits 151).  Eight waves serve a grid of less than
+// sequences of 4096 .. 16384: 1 split 209 us, 8 splits 151).  Eight waves serve a grid of at most
 // a workgroup per CU (509 tokens: 6.6 us against 7.1; 1024 workgroups of 512 tokens: 15.4 against 11.6).
 AttnPlan plan_rows(const AttnSize& n) {
     AttnPlan p{};
@@ -109,7 +109,7 @@ AttnPlan plan_rows(const AttnSize& n) {
         if (n.blocks > 96 * splits && groups < 4 * fit) splits = (n.blocks + 63) / 64;
     }
     finish_plan(p, n, splits);
-    p.waves = groups * p.splits < kCus ? 8 : 4;
+    p.waves = groups * p.splits <= kCus ? 8 : 4;
     p.us += 6.0f + (0.15f + 0.65f * n.dim / 128) * groups * n.mean / (4 * kCus);
     return p;
 }
