@@ -87,24 +87,20 @@ __host__ __device__ __forceinline__ constexpr int kv_tok(int q, int slot) {
     return 16 * (q >> 1) + 8 * (slot >> 2) + 4 * (q & 1) + (slot & 3);
 }
 
-// A word as four fp16 pairs of code + bias.  A nibble at bits 0..3 of a half under the exponent
+// A word as four fp16 pairs of code - 8, exactly.  A nibble at bits 0..3 of a half under the exponent
 // of 2^10 reads 1024 + code, one at bits 4..7 under that of 2^6 reads 64 + code: pairs 0 and 2 are
 // off by 1024 + 8, pairs 1 and 3 by 64 + 8, and one shift serves a word.
 constexpr float kBiasEven = 1032.0f, kBiasOdd = 72.0f;
-// The constants are held in registers, which makes a pair one v_and_or_b32: 5 VALU a word.
+// The constants are held in registers, which makes a biased pair one v_and_or_b32: 9 VALU a word.
 struct Unpack {
     uint32_t lo = 0x000F000Fu, hi = 0x00F000F0u, even = 0x64006400u, odd = 0x54005400u;
     __device__ __forceinline__ Unpack() {
         asm volatile("" : "+s"(lo), "+s"(hi));
         asm volatile("" : "+v"(even), "+v"(odd));
     }
-    __device__ __forceinline__ u4 biased(uint32_t w) const {
-        const uint32_t w8 = w >> 8;
-        return u4{(w & lo) | even, (w & hi) | odd, (w8 & lo) | even, (w8 & hi) | odd};
-    }
-    // code - 8, exactly
     __device__ __forceinline__ u4 values(uint32_t w) const {
-        const u4 b = biased(w);
+        const uint32_t w8 = w >> 8;
+        const u4 b = {(w & lo) | even, (w & hi) | odd, (w8 & lo) | even, (w8 & hi) | odd};
         const h2 e = {(_Float16)kBiasEven, (_Float16)kBiasEven}, o = {(_Float16)kBiasOdd, (_Float16)kBiasOdd};
         return u4{bitcast<uint32_t>(bitcast<h2>(b[0]) - e), bitcast<uint32_t>(bitcast<h2>(b[1]) - o),
                   bitcast<uint32_t>(bitcast<h2>(b[2]) - e), bitcast<uint32_t>(bitcast<h2>(b[3]) - o)};

@@ -149,8 +149,8 @@ struct QueryRow {
     }
 };
 
-// Waves a SIMD holds of the kernel of few rows: what its registers allow (97, 134, 164, 202 and 256
-// for 64 .. 256 channels: sums D / 4, queries D / 8, and their starts).
+// Waves a SIMD holds of the kernel of few rows: what its registers allow (89, 122, 148, 202 and 256
+// for 64 .. 256 channels: sums D / 4, queries D / 8).
 constexpr int kv_rows_waves(int D) { return D == 64 ? 4 : (D <= 128 ? 3 : 2); }
 
 // kv_rows.hip: `waves` (4 or 8) per workgroup, tiles of 16 rows.

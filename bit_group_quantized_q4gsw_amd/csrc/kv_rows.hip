@@ -9,9 +9,10 @@
 //   * scores: 16x16x32 MFMA, keys as the first operand, so a lane holds the scores of eight tokens
 //     of one row.  The codes enter as fp16 integers and every run of 32 channels is one MFMA, whose
 //     fp32 sum is multiplied by the token's scale: exact products (a scale multiplied into fp16
-//     codes would round, and scores feel that rounding most: twice the output's own).  Up to
-//     128 channels the codes keep the bias of their unpacking, which saves 4 of 9 VALU a word, and
-//     the product starts from -bias * sum(q) (wider rows leave no registers to hold that start).
+//     codes would round, and scores feel that rounding most: twice the output's own).  The codes are
+//     unpacked to their values: with the bias of their unpacking left in and taken out of the sum
+//     (4 of 9 VALU a word less) a sum would start a thousand times above its result, and queries whose
+//     channels have an offset in common lost up to 12 of its bits.
 //   * weights: running reference and sum of a softmax in fp32; the reference moves only when some
 //     score passes it by kSlack, so most blocks need no exchange between lanes and no rescaling.
 //   * sums: 16x16x32 MFMA, values' codes as the first operand; the second, which the lane holds
@@ -22,7 +23,7 @@
 //
 // Bound: HBM for long caches (36 * dim bytes per 32 tokens and head): 64 sequences of 4096 .. 16384
 // tokens, 8 heads of 128, 719 MB in 150 us, 4.8 TB/s (a large copy: 4.72).  At 128 channels a unit
-// costs some 260 VALU and 16 products a wave, 60% of the time its bytes take.  Short caches are
+// costs some 290 VALU and 16 products a wave, two thirds of the time its bytes take.  Short caches are
 // latency: 3 us to the first unit, 2 us for the waves' join, 4 to 5 us for the splits' join.
 #include "kv_attention.h"
 
@@ -55,7 +56,6 @@ __device__ __forceinline__ u2 word_pair(const uint8_t* plane, int g, int lane) {
 template <int D>
 __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnArgs a) {
     constexpr int G = D / 32, C = D / 16, kUnit = 36 * D, kLoads = (kUnit + 1023) / 1024;
-    constexpr bool kBiased = D <= 128;
     extern __shared__ __attribute__((aligned(16))) float smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -101,7 +101,6 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
 
     // ---- queries and the first block's unit: all loads in flight together ----
     u4 bq[G];
-    float cb[kBiased ? G : 1];           // -bias * sum of the run's queries
     const bool ok = i < nr;
     const int tok = ok ? (r0 + i) / a.group : 0, gh = ok ? r0 + i - tok * a.group : 0;
     const int place = ok ? s.len - s.m + tok : sp.pmax;
@@ -133,18 +132,6 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
 
     float f = a.scale * qr.convert(a.dtype, ok, wave_max_rows, bq);
     if (a.cap_out == 0.0f) f *= kLog2e;
-    if constexpr (kBiased) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const h2 p = bitcast<h2>(bq[g][e]);
-                sum = fmaf((float)p[0] + (float)p[1], (e & 1) ? kBiasOdd : kBiasEven, sum);
-            }
-            cb[g] = -wave_sum_rows(sum);
-        }
-    }
 
     f4 o[C];
     float mref = kNoKey, l = 0.0f;
@@ -166,12 +153,10 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
             if (g && (g & 3) == 0 && D >= 256) __builtin_amdgcn_sched_barrier(0);
             const u2 kw = word_pair<G>(unit, g, lane);
             const u4 ks = *reinterpret_cast<const u4*>(unit + 1024 * G + (qd * G + g) * 16);
-            const float c0 = kBiased ? cb[g] : 0.0f;
 #pragma unroll
             for (int ab = 0; ab < 2; ++ab) {
-                const u4 kf = kBiased ? unpack.biased(kw[ab]) : unpack.values(kw[ab]);
                 const h2 s01 = bitcast<h2>(ks[2 * ab]), s23 = bitcast<h2>(ks[2 * ab + 1]);
-                const f4 p = mfma_f16(kf, bq[g], f4{c0, c0, c0, c0});
+                const f4 p = mfma_f16(unpack.values(kw[ab]), bq[g], f4{0.f, 0.f, 0.f, 0.f});
                 sc[ab][0] = fmaf((float)s01[0], p[0], sc[ab][0]);
                 sc[ab][1] = fmaf((float)s01[1], p[1], sc[ab][1]);
                 sc[ab][2] = fmaf((float)s23[0], p[2], sc[ab][2]);
