@@ -29,6 +29,13 @@ constexpr float kNoKey = -3.0e38f;   // reference exponent of a row that has see
 // largest weight of a row is at least 2^kLift, 2^30 times fp16's smallest step.
 constexpr float kLift = 6.0f, kSlack = 8.0f;
 
+// The last place that the window of the row at `place` has left behind; -1: none (no window, or a row
+// nearer to the start than the window is long; places may be negative and windows as long as an
+// int: their difference may not fit one).
+__device__ __forceinline__ int kv_left_behind(const KvAttnArgs& a, int place) {
+    return a.window && place >= a.window ? place - a.window : -1;
+}
+
 // What the rows [r0, r0 + nr) of one (sequence, cache head) see: row r is new token r / group,
 // query head r % group; its place is p0 + r / group.
 struct KvSpan {

@@ -197,7 +197,7 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
 
     auto compute = [&](int t, uint32_t gone_blocks) {
         const int t0 = (int)(32 * (sp.lo + t * TB));
-        if (!active || t0 > wmax || (a.window && t0 + 32 * TB - 1 <= wmin - a.window)) return;
+        if (!active || t0 > wmax || t0 + 32 * TB - 1 <= kv_left_behind(a, wmin)) return;
         const uint8_t* stage = lds + (t & 1) * kStage;
         f32x16 sc[TB];
 #pragma unroll
@@ -228,8 +228,8 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
             }
             fl = 1.0f;
         }
-        if (t0 + 32 * TB - 1 > wmin || (a.window && t0 <= wmax - a.window) || gone_blocks) {
-            const int gone = a.window ? place - a.window : -1;
+        if (t0 + 32 * TB - 1 > wmin || t0 <= kv_left_behind(a, wmax) || gone_blocks) {
+            const int gone = kv_left_behind(a, place);
 #pragma unroll
             for (int u = 0; u < TB; ++u) {
                 const bool bad = (gone_blocks >> u) & 1;

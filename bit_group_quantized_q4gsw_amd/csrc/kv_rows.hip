@@ -165,7 +165,7 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
         }
         const int t0 = (int)(32 * blk);
         const int tl = t0 + 16 * (qd >> 1) + 4 * (qd & 1);     // + 8 ab + j
-        const bool edge = t0 + 31 > sp.pmin || (a.window && t0 <= sp.pmax - a.window);
+        const bool edge = t0 + 31 > sp.pmin || t0 <= kv_left_behind(a, sp.pmax);
         const bool tail = t0 + 32 > s.len;
         if (tail) {
             // places past the length may hold anything: their values' scales become 0 in the stage
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
             fl = 1.0f;
         }
         if (edge) {
-            const int gone = a.window ? place - a.window : -1;
+            const int gone = kv_left_behind(a, place);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int t = tl + 8 * (e >> 2) + (e & 3);

@@ -427,8 +427,8 @@ q4gsw_status q4gsw_kv_bytes(const q4gsw_kv_cache *c, uint64_t *bytes);
 /*
  * The sequences of a call.  Sequence b owns token rows cu[b] .. cu[b + 1] - 1 of the call's token
  * arrays (cu device int32 [batch + 1], not decreasing); they are the last of the lens[b] (device int32
- * [batch]) tokens it has with them.  Its token at place p is in page table[b * table_ld + p / page_size]
- * (device int32).  A place before 0, past the table's table_cols columns or on a page number outside
+ * [batch], at most 2^31 - 64) tokens it has with them.  Its token at place p is in page
+ * table[b * table_ld + p / page_size] (device int32).  A place before 0, past the table's table_cols columns or on a page number outside
  * [0, pages) is no place: nothing is stored there, it reads as zeros and attention does not see it.
  * Token rows that belong to no sequence are not touched (attention: left undefined).
  */

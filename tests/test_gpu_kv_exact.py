@@ -86,7 +86,7 @@ def check(got, want, bound, label, limit=None):
     err = (g - want).abs()
     off = rms(err, want)
     print(f"{label}: rms {off:.2e}, worst {float((err / bound).max()):.3f} of the bound", flush=True)
-    assert (err <= bound).all(), f"{label}: {int((err > bound).sum())} elements past the bound, rms {off:.2e}"
+    assert bool((err <= bound).all()), f"{label}: {int((err > bound).sum())} elements past the bound, rms {off:.2e}"
     assert off <= (limit or rms_limit(got.dtype)), f"{label}: rms error {off:.2e}"
 
 
@@ -112,3 +112,23 @@ def test_queries_with_a_common_offset(kernel, dtype, dim, common):
     with q.forced_kv_kernel(kernel):
         got = q.kv_attention(cache, x.to(dtype).cuda(), table, offsets(news), ln, max(news), max(lens))
     check(got, want, bound, f"offset {common}")
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_window_of_any_size_with_rows_before_place_0(kernel, dtype):
+    """The largest window an int32 holds is no window at all, also for a wave whose first rows are at
+    places before 0."""
+    q = lib()
+    news, length, before, hq, hkv, dim = [80], 70, 10, 4, 1, 64
+    cache, table, _, keys, values = stored(q, [length], hkv, dim, 32, dtype, 3)
+    x = torch.randint(-4, 5, (80, hq, dim), generator=torch.Generator().manual_seed(1)).to(dtype)
+    ln = torch.tensor([length], dtype=torch.int32, device="cuda")
+    for window in (2 ** 31 - 1, 2 ** 31 - 5, 2 ** 31 - 80, 71, 33):
+        print(f"window {window} {kernel} {dtype}", flush=True)
+        want, bound = expected(x[before:], keys, values, [length], [length], window)
+        sharp(want[8:], bound[8:])
+        with q.forced_kv_kernel(kernel):
+            got = q.kv_attention(cache, x.cuda(), table, offsets(news), ln, 80, length, window=window)
+        assert not got[:before].any()
+        check(got[before:], want, bound, f"window {window}")
