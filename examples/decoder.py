@@ -6,12 +6,13 @@ Every layer is
     cache  <- k, v;  y = attention(q, cache)       kv_append, kv_attention
     h, rows = h + y . Wo^T, int8 rows of its norm  linear_fwd, rmsnorm_dq8ca
     y = (silu(g) * u) . Wd^T, [g u] = rows . Wu^T  linear_dq8ca_rows, linear_fwd
-on random weights.  Run as a command it takes a batch of prompts of unlike lengths in one call and
-then decodes from a captured HIP graph:
+on random weights, without positions (nothing rotates q and k on their way).  Run as a command it
+takes a batch of prompts of unlike lengths in one call and then decodes from a captured HIP graph:
 
     python examples/decoder.py [--layers 4] [--batch 8] [--prompt 512] [--tokens 64]
 """
 import argparse
+import copy
 import os
 import sys
 import time
@@ -77,7 +78,7 @@ class Decoder:
 
 class State:
     """The sequences of a batch: a cache per layer, the page table, and the lengths with the call's
-    new tokens."""
+    new tokens.  The tensors stay where they are: a captured graph holds their addresses."""
 
     def __init__(self, c, capacity):
         need = [(n + PAGE - 1) // PAGE for n in capacity]
@@ -89,40 +90,59 @@ class State:
         self.table = table.cuda()
         self.caches = [q.kv_cache(pages, PAGE, c.kv_heads, c.dim) for _ in range(c.layers)]
         self.lens = torch.zeros(len(need), dtype=torch.int32, device="cuda")
-        self.cu = None
+        self.cu = torch.zeros(len(need) + 1, dtype=torch.int32, device="cuda")
+        self.capacity, self.held = list(capacity), [0] * len(need)
+
+    def take(self, news):
+        """Count news[b] more tokens of sequence b on the host; ValueError if one has no room for them."""
+        held = [n + m for n, m in zip(self.held, news)]
+        for b, (n, room) in enumerate(zip(held, self.capacity)):
+            if n > room:
+                raise ValueError(f"sequence {b} has room for {room} tokens, {n} needed")
+        self.held[:] = held
 
     def advance(self, news):
         """The next call brings news[b] tokens of sequence b."""
-        self.cu = torch.tensor([sum(news[:b]) for b in range(len(news) + 1)], dtype=torch.int32, device="cuda")
+        self.take(news)
+        self.cu.copy_(torch.tensor([sum(news[:b]) for b in range(len(news) + 1)], dtype=torch.int32))
         self.lens += torch.tensor(news, dtype=torch.int32, device="cuda")
 
 
 class Stepper:
-    """One greedy token of every sequence a replay, from a captured graph."""
+    """One greedy token of every sequence a replay, from a captured graph.  `ids` holds the next step's
+    tokens; between steps the state may take prompt chunks."""
 
     def __init__(self, model, state, ids, max_ctx):
         self.model, self.state, self.max_ctx = model, state, max_ctx
         self.ids = ids.clone()
         batch = ids.numel()
-        state.advance([1] * batch)
-        self.ones = torch.ones_like(state.lens)
+        self.view = copy.copy(state)             # the state's tensors, with the offsets of single tokens
+        self.view.cu = torch.arange(batch + 1, dtype=torch.int32, device="cuda")
         self.last = torch.arange(batch, device="cuda")
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
-        with torch.cuda.stream(side):        # writes the places that the first replay writes again
-            self.model.logits(self.ids, state, 1, max_ctx, self.last)
+        with torch.cuda.stream(side):        # writes the places that the first step writes again
+            state.lens.add_(1)
+            self.model.logits(self.ids, self.view, 1, max_ctx, self.last)
+            state.lens.sub_(1)
         torch.cuda.current_stream().wait_stream(side)
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph):
-            self.out = self.step()
+            self.out = self.launch()
 
-    def step(self):
-        out = self.model.logits(self.ids, self.state, 1, self.max_ctx, self.last)
+    def launch(self):
+        self.state.lens.add_(1)
+        out = self.model.logits(self.ids, self.view, 1, self.max_ctx, self.last)
         self.ids.copy_(out.argmax(1))
-        self.state.lens.add_(self.ones)
         return out
 
+    def step(self):
+        """The same step without the graph."""
+        self.state.take([1] * self.ids.numel())
+        return self.launch()
+
     def __call__(self):
+        self.state.take([1] * self.ids.numel())
         self.graph.replay()
         return self.out
 
