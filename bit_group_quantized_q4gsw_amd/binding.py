@@ -149,6 +149,8 @@ def lib() -> ctypes.CDLL:
             "q4gsw_rmsnorm_dq8ca": [vp, i32, vp, vp, i32, i64, i64, ctypes.c_float, vp, vp, u64, vp, vp],
             "q4gsw_dq8ca_rows_workspace_bytes": [pw, i64, ctypes.POINTER(u64)],
             "q4gsw_linear_dq8ca_rows": [pw, vp, u64, i64, vp, vp, u64, vp],
+            "q4gsw_dq8ca_rows_workspace_bytes_ex": [pw, i64, po, ctypes.POINTER(u64)],
+            "q4gsw_linear_dq8ca_rows_ex": [pw, vp, u64, i64, vp, vp, u64, po, vp],
             "q4gsw_kv_bytes": [pc, ctypes.POINTER(u64)],
             "q4gsw_kv_append": [pc, ps, vp, i64, vp, i64, i32, vp],
             "q4gsw_kv_read": [pc, ps, vp, vp, vp],
@@ -445,10 +447,11 @@ def linear_dq8ca_rows(w: PackedWeight, rows: Dq8caRows, out: Optional[torch.Tens
     dev = rows.buffer.device
     y = _out(out, (rows.M, w.N), dev, "out")
     need = ctypes.c_uint64()
-    _check(lib().q4gsw_dq8ca_rows_workspace_bytes(w.ref(), rows.M, ctypes.byref(need)), "q4gsw_dq8ca_rows_workspace_bytes")
+    _check(lib().q4gsw_dq8ca_rows_workspace_bytes_ex(w.ref(), rows.M, _opts(), ctypes.byref(need)),
+           "q4gsw_dq8ca_rows_workspace_bytes")
     ws, wp, wb = _ws_args(need.value, workspace, dev)
-    _check(lib().q4gsw_linear_dq8ca_rows(w.ref(), rows.buffer.data_ptr(), rows.buffer.numel(), rows.M, y.data_ptr(), wp,
-                                         wb, _stream()), "q4gsw_linear_dq8ca_rows")
+    _check(lib().q4gsw_linear_dq8ca_rows_ex(w.ref(), rows.buffer.data_ptr(), rows.buffer.numel(), rows.M, y.data_ptr(),
+                                            wp, wb, _opts(), _stream()), "q4gsw_linear_dq8ca_rows")
     return y
 
 

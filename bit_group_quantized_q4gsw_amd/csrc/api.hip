@@ -522,22 +522,31 @@ q4gsw_status q4gsw_dq8ca_rows_bytes(int64_t M, int64_t K, uint64_t* bytes) {
     return Q4GSW_OK;
 }
 
-q4gsw_status q4gsw_dq8ca_rows_workspace_bytes(const q4gsw_weight* w, int64_t M, uint64_t* bytes) {
+q4gsw_status q4gsw_dq8ca_rows_workspace_bytes_ex(const q4gsw_weight* w, int64_t M, const q4gsw_options* opts,
+                                                 uint64_t* bytes) {
     if (!bytes) return Q4GSW_E_NULL;
-    const q4gsw_status st = check_desc(w);
+    q4gsw_status st = check_desc(w);
     if (st != Q4GSW_OK) return st;
     if (M < 1 || M > kMaxM) return Q4GSW_E_SHAPE;
+    Opts o;
+    if ((st = read_opts(opts, &o)) != Q4GSW_OK) return st;
     const WView v = view_of(w);
     if (!dq8ca_supported(v)) return Q4GSW_E_GROUP;
-    *bytes = (uint64_t)plan_dq8ca(v, M).ws_bytes - dq8ca_rows_total(M, w->K);
+    *bytes = (uint64_t)plan_dq8ca(v, M, o.splits).ws_bytes - dq8ca_rows_total(M, w->K);
     return Q4GSW_OK;
 }
 
-q4gsw_status q4gsw_linear_dq8ca_rows(const q4gsw_weight* w, const void* rows, uint64_t rows_bytes, int64_t M, float* y,
-                                     void* ws, uint64_t ws_bytes, void* stream) {
+q4gsw_status q4gsw_dq8ca_rows_workspace_bytes(const q4gsw_weight* w, int64_t M, uint64_t* bytes) {
+    return q4gsw_dq8ca_rows_workspace_bytes_ex(w, M, nullptr, bytes);
+}
+
+q4gsw_status q4gsw_linear_dq8ca_rows_ex(const q4gsw_weight* w, const void* rows, uint64_t rows_bytes, int64_t M, float* y,
+                                        void* ws, uint64_t ws_bytes, const q4gsw_options* opts, void* stream) {
     uint64_t need = 0;
-    q4gsw_status st = q4gsw_dq8ca_rows_workspace_bytes(w, M, &need);
+    q4gsw_status st = q4gsw_dq8ca_rows_workspace_bytes_ex(w, M, opts, &need);
     if (st != Q4GSW_OK) return st;
+    Opts o;
+    if ((st = read_opts(opts, &o)) != Q4GSW_OK) return st;
     if (!rows || !y) return Q4GSW_E_NULL;
     const uint64_t total = dq8ca_rows_total(M, w->K);
     if (rows_bytes < total) return Q4GSW_E_BUFFER;
@@ -547,8 +556,13 @@ q4gsw_status q4gsw_linear_dq8ca_rows(const q4gsw_weight* w, const void* rows, ui
     const Range sr = range_of(ws, need);
     if (overlap(yr, rr) || overlap(yr, wr) || overlap(sr, yr) || overlap(sr, rr) || overlap(sr, wr)) return Q4GSW_E_ALIAS;
     const WView v = view_of(w);
-    return hip_status(launch_dq8ca_rows(v, dq8ca_rows_at(const_cast<void*>(rows), M, w->K), M, y, plan_dq8ca(v, M), ws,
-                                        static_cast<hipStream_t>(stream)));
+    return hip_status(launch_dq8ca_rows(v, dq8ca_rows_at(const_cast<void*>(rows), M, w->K), M, y,
+                                        plan_dq8ca(v, M, o.splits), ws, static_cast<hipStream_t>(stream)));
+}
+
+q4gsw_status q4gsw_linear_dq8ca_rows(const q4gsw_weight* w, const void* rows, uint64_t rows_bytes, int64_t M, float* y,
+                                     void* ws, uint64_t ws_bytes, void* stream) {
+    return q4gsw_linear_dq8ca_rows_ex(w, rows, rows_bytes, M, y, ws, ws_bytes, nullptr, stream);
 }
 
 q4gsw_status q4gsw_qkv_fused_ex(const q4gsw_weight* wq, const q4gsw_weight* wk, const q4gsw_weight* wv, const void* x,

@@ -403,6 +403,12 @@ q4gsw_status q4gsw_rmsnorm_dq8ca(const void *x, int32_t x_dtype, const void *res
 q4gsw_status q4gsw_dq8ca_rows_workspace_bytes(const q4gsw_weight *w, int64_t M, uint64_t *bytes);
 q4gsw_status q4gsw_linear_dq8ca_rows(const q4gsw_weight *w, const void *rows, uint64_t rows_bytes, int64_t M,
                                      float *y, void *ws, uint64_t ws_bytes, void *stream);
+/* Both with per-call options (only `splits` applies; NULL: the same calls). */
+q4gsw_status q4gsw_dq8ca_rows_workspace_bytes_ex(const q4gsw_weight *w, int64_t M, const q4gsw_options *opts,
+                                                 uint64_t *bytes);
+q4gsw_status q4gsw_linear_dq8ca_rows_ex(const q4gsw_weight *w, const void *rows, uint64_t rows_bytes, int64_t M,
+                                        float *y, void *ws, uint64_t ws_bytes, const q4gsw_options *opts,
+                                        void *stream);
 
 /*
  * A paged cache of keys and values in 4 bits: `pages` pages of page_size tokens (a power of two,
