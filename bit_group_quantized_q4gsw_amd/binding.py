@@ -466,8 +466,16 @@ class KvCache:
         self._dev = buffer.get_device()
 
 
+def _int32(*sizes: int) -> None:
+    """ctypes takes integers modulo 2^32 without a word."""
+    for n in sizes:
+        if n >> 31 not in (0, -1):
+            raise ValueError(f"{n} does not fit a 32-bit argument")
+
+
 def kv_cache(pages: int, page_size: int, heads: int, dim: int, device="cuda") -> KvCache:
     """An empty cache (zeros) of `pages` pages of page_size tokens."""
+    _int32(page_size, heads, dim)
     desc = KvCacheDesc(pages, page_size, heads, dim, 0, None, 0)
     out = ctypes.c_uint64()
     _check(lib().q4gsw_kv_bytes(ctypes.byref(desc), ctypes.byref(out)), "q4gsw_kv_bytes")
@@ -551,6 +559,7 @@ def kv_read(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, lens: torch.T
 
 def kv_attention_workspace_bytes(cache: KvCache, batch: int, tokens: int, hq: int, max_new: int, max_ctx: int) -> int:
     """Workspace of kv_attention calls with these sizes (any window)."""
+    _int32(batch, hq, max_new, max_ctx)
     out = ctypes.c_uint64()
     _check(lib().q4gsw_kv_attention_workspace_bytes(cache._ref, batch, tokens, hq, max_new, max_ctx, ctypes.byref(out)),
            "q4gsw_kv_attention_workspace_bytes")
@@ -561,6 +570,7 @@ def kv_attention_plan(cache: KvCache, batch: int, tokens: int, hq: int, max_new:
                       dtype: torch.dtype, window: int = 0) -> dict:
     """How a kv_attention call with these sizes runs: the kernel ("few_rows" or "many_rows"), waves
     per workgroup and splits of the cache's length."""
+    _int32(batch, hq, max_new, max_ctx, window)
     info = KvPlanInfo()
     _check(lib().q4gsw_kv_attention_plan(cache._ref, batch, tokens, hq, max_new, max_ctx, window, _TORCH_DTYPE[dtype],
                                          _local.kv, ctypes.byref(info)), "q4gsw_kv_attention_plan")
@@ -573,6 +583,8 @@ def kv_attention(cache: KvCache, q: torch.Tensor, table: torch.Tensor, cu: torch
     """out [tokens, hq, dim] of q's dtype: causal attention of the new tokens q over the cache, which
     holds their own keys and values already.  max_new and max_ctx bound the sequences' new tokens and
     lengths; window > 0 keeps the last `window` keys of each token, softcap > 0 caps the scores."""
+    if (max_new | max_ctx | window) >> 31:       # negative ones too, of which the library refuses the 32-bit ones
+        _int32(max_new, max_ctx, window)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, hq, dim]")
     shape = q.shape
