@@ -1,4 +1,4 @@
-// Shared by the attention kernels over the 4-bit cache (kv_rows.hip, kv_prompt.hip, kv_join.hip).
+// Shared by the attention kernels over the 4-bit cache (kv_rows.hip, kv_prompt.hip).
 #pragma once
 #include "kv4.h"
 
@@ -159,6 +159,17 @@ struct QueryRow {
 // Waves a SIMD holds of the kernel of few rows: what its registers allow (89, 122, 148, 202 and 256
 // for 64 .. 256 channels: sums D / 4, queries D / 8).
 constexpr int kv_rows_waves(int D) { return D == 64 ? 4 : (D <= 128 ? 3 : 2); }
+
+// The kernel of many rows: blocks of 32 tokens in a tile (two, but one where two with the remainders
+// that `prec` keeps do not fit LDS twice), bytes of its two stages of keys and values, and how many of
+// its workgroups of `waves` a CU of 160 KB holds: registers allow two waves a SIMD up to 128 channels and one
+// above.
+constexpr int prompt_blocks(int D, bool prec) { return prec && D > 128 ? 1 : 2; }
+constexpr int prompt_lds(int D, bool prec) { return 2 * prompt_blocks(D, prec) * (D / 16) * 1024 * (prec ? 4 : 2); }
+constexpr int prompt_fit(int D, bool prec, int waves) {
+    const int by_regs = (D <= 128 ? 8 : 4) / waves, by_lds = 160 * 1024 / prompt_lds(D, prec);
+    return by_regs < by_lds ? by_regs : by_lds;
+}
 
 // kv_rows.hip: `waves` (4 or 8) per workgroup, tiles of 16 rows.
 hipError_t launch_kv_rows(const KvAttnArgs& a, int waves, hipStream_t s);

@@ -50,9 +50,6 @@ __device__ __forceinline__ int by_length(const KvSeqs& sq, int rank, int lane) {
     return __builtin_ctzll(__ballot(before == rank));
 }
 
-// Blocks of 32 tokens in a tile: two, but one where two with remainders do not fit LDS twice.
-constexpr int prompt_blocks(int D, bool prec) { return prec && D > 128 ? 1 : 2; }
-
 template <int D, int NW, bool PREC>
 __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(KvAttnArgs a) {
     constexpr int G = D / 32, S = D / 16, TB = prompt_blocks(D, PREC);
@@ -352,7 +349,7 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
 
 template <int D, int NW, bool PREC>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
-    constexpr int lds = 2 * prompt_blocks(D, PREC) * (D / 16) * 1024 * (PREC ? 4 : 2);
+    constexpr int lds = prompt_lds(D, PREC);
     const int64_t blocks = (int64_t)a.splits * a.c.heads * a.sq.batch * a.row_tiles;
     hipLaunchKernelGGL((kv_prompt_kernel<D, NW, PREC>), dim3((unsigned)blocks), dim3(64 * NW), lds, s, a);
     return hipGetLastError();

@@ -98,6 +98,8 @@ void finish_plan(AttnPlan& p, const AttnSize& n, int64_t splits) {
 // splits and few turns, unlike lengths end at unlike times, and shorter splits balance them (64
 // sequences of 4096 .. 16384: 1 split 209 us, 8 splits 151).  Eight waves serve a grid of at most
 // a workgroup per CU (509 tokens: 6.6 us against 7.1; 1024 workgroups of 512 tokens: 15.4 against 11.6).
+// The estimate: time of a tile of 16 rows by 32 keys on a CU, of which a grid that fits at once gives the
+// fullest CU a whole number, and of a workgroup's loads and join.
 AttnPlan plan_rows(const AttnSize& n) {
     AttnPlan p{};
     p.row_tiles = (n.rows + 15) / 16;
@@ -110,25 +112,58 @@ AttnPlan plan_rows(const AttnSize& n) {
     }
     finish_plan(p, n, splits);
     p.waves = groups * p.splits <= kCus ? 8 : 4;
-    p.us += 6.0f + (0.15f + 0.65f * n.dim / 128) * groups * n.mean / (4 * kCus);
+    const float turns = (float)groups * p.splits / fit;
+    const float per_cu = turns <= 1 ? (float)((groups * p.splits + kCus - 1) / kCus) : (float)groups * p.splits / kCus;
+    p.us += 4.0f + (0.085f + 0.0045f * n.dim) * per_cu * n.mean / (4 * p.splits) + (2.0f + 0.026f * n.dim) * (turns < 1 ? 1 : turns);
     return p;
 }
 
-// Many rows: eight waves share a tile's unpacking where that still gives every CU a workgroup
-// (wider heads have registers for one wave a SIMD).
+// us of a turn of 64 keys of a workgroup that fills its CU (eight waves up to 128 channels, four above).
+float prompt_turn(int dim, bool prec) {
+    if (dim <= 128) return prec ? 0.66f + 0.0235f * dim : 0.65f + 0.0135f * dim;
+    return prec ? 0.8f + 0.0211f * dim : 0.47f + 0.013f * dim;
+}
+
+// Most splits of the kernel of many rows with `waves` a workgroup: of 16 blocks at least, and as many as
+// keep every workgroup of the grid on the GPU at once.  One more launches a second turn of workgroups
+// and halves what each has to do (32 / 8 heads of 128, bf16, `waves` 8: 2048 tokens, 256 workgroups: 74 us,
+// 2 splits 106; 1024 behind 7000, 128 workgroups: 2 splits 161 us, 1 split 237, 3 splits 198).
+int64_t prompt_splits(const AttnSize& n, int waves, bool prec) {
+    const int64_t groups = (int64_t)n.batch * n.heads * ((n.rows + 32 * waves - 1) / (32 * waves));
+    const int64_t fill = kCus * prompt_fit(n.dim, prec, waves) / groups, most = (n.blocks + 15) / 16;
+    const int64_t splits = fill < most ? fill : most;
+    return splits < 1 ? 1 : splits;
+}
+
+// Many rows: eight waves (up to 128 channels), which share a tile's unpacking, or four, and keys split as far
+// as the grid fits or not at all, by the estimate: a workgroup's own turns, or all turns over the CUs.  Of workgroups of
+// four waves that fit a CU twice two take 1.3 times the turn of one of eight waves, and one alone 0.85 times.  Prompts
+// from their beginning have rows of unlike lengths, which splits balance badly (1024 tokens, 32 / 8 heads of 128, bf16: four
+// waves 37.5 us, 2 splits 47; eight waves 41 and 45); few rows need them (256 tokens behind 3744: eight waves
+// and 8 splits 46 us, 4 splits 53, 1 split 124).
 AttnPlan plan_prompt(const AttnSize& n) {
-    AttnPlan p{};
-    p.prompt = true;
-    p.waves = n.dim <= 128 && (int64_t)n.batch * n.heads * ((n.rows + 255) / 256) >= kCus ? 8 : 4;
-    p.row_tiles = (n.rows + 32 * p.waves - 1) / (32 * p.waves);
-    const int64_t groups = (int64_t)n.batch * n.heads * p.row_tiles;
-    const int64_t fill = (kCus * 3 / 2 + groups - 1) / groups, most = (n.blocks + 15) / 16;
-    finish_plan(p, n, fill < most ? fill : most);
-    // 64 keys are a turn; a workgroup's own turns, and all turns over the CUs (two groups of four waves each)
-    const float longest = (n.dim <= 128 ? 3.3f : 9.0f) * 0.5f * p.chunk;
-    const float all = (1.0f + 1.6f * n.dim / 128) * 0.5f * groups * n.mean / (kCus * (p.waves == 8 ? 1 : 2));
-    p.us += 8.0f + (n.prec ? 1.5f : 1.0f) * (longest > all ? longest : all);
-    return p;
+    AttnPlan best{};
+    for (int waves = n.dim <= 128 ? 8 : 4; waves >= 4; waves -= 4) {
+        AttnPlan p{};
+        p.prompt = true;
+        p.waves = waves;
+        p.row_tiles = (n.rows + 32 * waves - 1) / (32 * waves);
+        const int64_t groups = (int64_t)n.batch * n.heads * p.row_tiles, most = prompt_splits(n, waves, n.prec);
+        const int fit = prompt_fit(n.dim, n.prec, waves);
+        const bool half = waves == 4 && n.dim <= 128;
+        for (int64_t splits = 1;; splits = most) {
+            finish_plan(p, n, splits);
+            float turns = (float)groups * p.splits / (kCus * fit);
+            const float whole = 0.9f * ((groups * p.splits + kCus * fit - 1) / (kCus * fit));
+            if (fit == 1 && turns < whole) turns = whole;            // a last turn that fills few CUs
+            const float all = (half ? (fit == 2 ? 1.3f : 0.85f) : 1.0f) * turns * 0.5f * n.mean / p.splits;
+            const float longest = (half ? 0.85f : 1.0f) * 0.5f * p.chunk;
+            p.us += 6.0f + prompt_turn(n.dim, n.prec) * (longest > all ? longest : all);
+            if (best.waves == 0 || p.us < best.us) best = p;
+            if (splits >= most) break;
+        }
+    }
+    return best;
 }
 
 AttnSize attention_size(int heads, int dim, int batch, int hq, int max_new, int max_ctx, int window, int dtype) {
@@ -145,12 +180,12 @@ AttnSize attention_size(int heads, int dim, int batch, int hq, int max_new, int 
     return n;
 }
 
-// Many rows share a tile's unpacking but take 64 keys in turn after turn, few rows spread over the
-// GPU; which is faster is estimated from the keys a row sees, with the times of one turn and of one
-// tile of 16 rows by 32 keys on the busy GPU (prompts of 32 / 8 heads of 128 from their beginning, few
-// against many rows: 512 tokens 18 against 23 us, 1024 tokens 40 against 56, 2048 tokens 111 against
-// 127, two of 2048 tokens 203 against 94; 1024 tokens behind 7000: 367 against 185).  Up to 32 rows
-// never fill the workgroup of many.
+// Many rows share a tile's unpacking but take 64 keys in turn after turn, few rows spread over the GPU;
+// which is faster is estimated.  us measured, few against many rows, in bf16 (in fp16; fp32 is within 3% of it), prompts
+// from their beginning of 32 / 8 heads of 128: 512 tokens 19 / 23 (18 / 27), 1024 tokens 42 / 38 (42 / 48), 2048 tokens
+// 118 / 71 (119 / 97), two of 2048 tokens 223 / 98 (219 / 137); 1024 tokens behind 7000 377 / 161 (372 / 234); of 16 / 4 heads
+// of 256: 2048 tokens 129 / 127 (130 / 198), two of 2048 tokens 235 / 152 (231 / 234), three chunks of 2048 behind 6144
+// 1732 / 1262 (1735 / 2026).  Up to 32 rows never fill the workgroup of many.
 AttnPlan plan_attention(const AttnSize& n, int kernel) {
     if (kernel == Q4GSW_KV_MANY_ROWS) return plan_prompt(n);
     const AttnPlan few = plan_rows(n);
@@ -260,11 +295,14 @@ q4gsw_status q4gsw_kv_attention_workspace_bytes(const q4gsw_kv_cache* c, int32_t
     q4gsw_status st = check_cache_shape(c);
     if (st != Q4GSW_OK) return st;
     if ((st = check_attention(c, batch, tokens, hq, max_new, max_ctx)) != Q4GSW_OK) return st;
-    // a window changes the span of keys, with which either plan's splits grow, and may change the plan
+    // the window and the type may change the plan; the splits of either kernel grow with the span of keys
     const AttnSize n = attention_size(c->heads, c->dim, batch, hq, max_new, max_ctx, 0, kBF16);
-    const uint64_t few = plan_workspace(plan_rows(n), tokens, hq, c->dim);
-    const uint64_t many = n.rows <= kFewRows ? 0 : plan_workspace(plan_prompt(n), tokens, hq, c->dim);
-    *bytes = few > many ? few : many;
+    AttnPlan most = plan_rows(n);
+    for (int i = 0; i < 4 && n.rows > kFewRows; ++i) {
+        const int64_t splits = prompt_splits(n, i & 1 ? 8 : 4, i & 2);
+        if (splits > most.splits) most.splits = (int)splits;
+    }
+    *bytes = plan_workspace(most, tokens, hq, c->dim);
     return Q4GSW_OK;
 }
 
