@@ -582,7 +582,8 @@ def kv_attention(cache: KvCache, q: torch.Tensor, table: torch.Tensor, cu: torch
                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """out [tokens, hq, dim] of q's dtype: causal attention of the new tokens q over the cache, which
     holds their own keys and values already.  max_new and max_ctx bound the sequences' new tokens and
-    lengths; window > 0 keeps the last `window` keys of each token, softcap > 0 caps the scores."""
+    lengths; window > 0 keeps the last `window` keys of each token, softcap > 0 caps the scores.  A row that
+    sees no key gives zeros, else one whose query holds a NaN or an infinity gives NaN."""
     if (max_new | max_ctx | window) >> 31:       # negative ones too, of which the library refuses the 32-bit ones
         _int32(max_new, max_ctx, window)
     if q.dim() != 3:

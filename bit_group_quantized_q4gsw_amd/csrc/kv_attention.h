@@ -59,11 +59,13 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs& a, const KvSeq& s, i
 
 // Factor 2^(14 - e), e the exponent of a row's largest magnitude, that brings the row into fp16's
 // range (every bf16 or fp16 value of it down to 2^-19 of the largest stays exact; fp32 values
-// round to 11 bits), and its inverse.  A zero row gets any factor, infinities and NaN stay.
+// round to 11 bits), and its inverse.  A zero row gets any factor; NaN stay, and an infinity makes the
+// whole row NaN: its scores would be infinite or NaN, and where all that a row sees are -inf the weights
+// would add up to 0, as if it saw no key.
 __device__ __forceinline__ void row_factor(float amax, float& mul, float& inv) {
     int eb = (int)(bitcast<uint32_t>(amax) >> 23) & 0xFF;
     eb = eb < 15 ? 15 : eb;
-    mul = bitcast<float>((uint32_t)(268 - eb > 254 ? 254 : 268 - eb) << 23);
+    mul = eb == 255 ? __builtin_nanf("") : bitcast<float>((uint32_t)(268 - eb > 254 ? 254 : 268 - eb) << 23);
     inv = bitcast<float>((uint32_t)(eb - 14) << 23);
 }
 

@@ -464,7 +464,8 @@ q4gsw_status q4gsw_kv_read(const q4gsw_kv_cache *c, const q4gsw_kv_seqs *s, floa
  * Causal attention of the new tokens over the cache:
  *   x[t] = q . k[t] / sqrt(dim);  with softcap > 0: x = softcap * tanh(x / softcap);
  *   out = sum_t softmax(x)[t] v[t] over t <= the token's place and, with window > 0, t > place - window.
- * A row that sees no key gives zeros.  Query head h reads cache head h / (hq / heads).
+ * A row that sees no key gives zeros; else one whose query holds a NaN or an infinity gives NaN.
+ * Query head h reads cache head h / (hq / heads).
  *   q    device, token rows q_ld elements apart, each [hq][dim] dense, in dtype; 16-byte aligned, pitch a
  *        multiple of 16 bytes.  Held as fp16 after a power of two per row (exact for fp16 and bf16 down
  *        to 2^-19 of the row's largest; fp32 rounds to 2^-11)

@@ -182,6 +182,32 @@ def test_scores_along_the_cache(kernel, dtype, shape):
         assert off <= rms_limit(dtype) * 2 ** 0.5 + 16 * 2.0 ** -24 * 2.0 ** max(power, 0) * 40
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_infinite_queries(kernel, cap, sign):
+    """An infinite query's row is NaN where it sees a key (its scores are infinite or NaN, of which a
+    softmax makes NaN, also where all are -inf), under a cap too.  Rows that see no key stay zeros, other
+    rows what they are."""
+    q = lib()
+    print(f"infinite queries {kernel} cap={cap} {sign}", flush=True)
+    dim, length, before, hq = 64, 40, 2, 2
+    cache, table, _, keys, values = stored(q, [length], 1, dim, 64, F16, 5)
+    ln = torch.tensor([length], dtype=torch.int32, device="cuda")
+    m = length + before
+    x = torch.randint(-4, 5, (m, hq, dim), generator=torch.Generator().manual_seed(1)).to(F16)
+    fine, bound = expected(x[before:], keys, values, [length], [length], 0, cap)
+    bad = x.clone()
+    bad[::2, 0, 7] = sign * float("inf")         # of places -2, 0, 2, ...
+    with q.forced_kv_kernel(kernel):
+        got = q.kv_attention(cache, bad.cuda(), table, offsets([m]), ln, m, length, softcap=cap).cpu().double()
+    assert not got[:before].any()
+    got = got[before:]
+    assert got[::2, 0].isnan().all()
+    err = (got - fine).abs()
+    assert bool((err <= bound)[1::2].all()) and bool((err <= bound)[:, 1].all())
+
+
 # The rms limit is doubled below where few values of unlike sizes make up an output: their roundings
 # average less.
 def reloads(q, kernel, lens, news, hq, hkv, dim, dtype, waves, hole, window=0):
