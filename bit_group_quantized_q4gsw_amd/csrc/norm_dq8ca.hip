@@ -244,8 +244,9 @@ hipError_t norm_launch(const NormArgs& a, int r_dtype, int64_t M, hipStream_t s)
     uintptr_t bits = 0;
     for (const void* p : {a.x, a.residual, a.weight, (const void*)a.h, (const void*)a.values}) bits |= reinterpret_cast<uintptr_t>(p);
     const int64_t octs = a.K >> 3;
-    const bool vec = a.K % 8 == 0 && (bits & 15u) == 0 && octs <= (int64_t)kOcts * kMaxThreads;
     const unsigned nt = octs <= 256 * kOcts ? 256 : (octs <= 512 * kOcts ? 512 : 1024);
+    // a grid takes fewer than 2^32 threads: millions of wide rows take 256 a row
+    const bool vec = a.K % 8 == 0 && (bits & 15u) == 0 && octs <= (int64_t)kOcts * kMaxThreads && M * (int64_t)nt < (int64_t(1) << 32);
     const dim3 grid((unsigned)M), block(vec ? nt : 256u);
 #define Q4GSW_NORM(RT)                                                                  \
     if (vec) hipLaunchKernelGGL((norm_dq8ca_kernel<XT, RT>), grid, block, 0, s, a);       \

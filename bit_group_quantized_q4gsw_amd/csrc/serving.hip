@@ -8,7 +8,7 @@ using namespace q4gsw;
 
 namespace {
 
-constexpr int64_t kMaxBlocks = 0x7FFFFFFF;
+constexpr int64_t kMaxBlocks = 0x7FFFFFFF, kMaxThreads = 0xFFFFFFFF;
 constexpr float kMinCap = 1e-30f, kMaxCap = 1e30f;   // 1 / cap and cap log2(e) stay normal
 
 q4gsw_status check_cache_shape(const q4gsw_kv_cache* c) {
@@ -352,7 +352,10 @@ q4gsw_status q4gsw_kv_attention_ex(const q4gsw_kv_cache* c, const q4gsw_kv_seqs*
     const AttnPlan p = plan_attention(attention_size(c->heads, c->dim, s->batch, hq, max_new, max_ctx, window, dtype),
                                       kernel);
     const uint64_t need = plan_workspace(p, s->tokens, hq, c->dim);
-    if ((int64_t)p.splits * p.row_tiles > kMaxBlocks / ((int64_t)s->batch * c->heads)) return Q4GSW_E_SHAPE;
+    // a grid takes fewer than 2^32 threads in one dimension; the join has up to 256 a row
+    if ((int64_t)p.splits * p.row_tiles > kMaxThreads / (64 * p.waves * ((int64_t)s->batch * c->heads)) ||
+        (p.splits > 1 && s->tokens * hq > kMaxThreads / 256))
+        return Q4GSW_E_SHAPE;
     if (!ws_ok(ws, ws_bytes, need)) return Q4GSW_E_WORKSPACE;
     const Range qr = range_of(q, rows_extent(s->tokens, q_ld, row, es));
     const Range orr = range_of(out, (uint64_t)s->tokens * row * es), sr = range_of(ws, need);
