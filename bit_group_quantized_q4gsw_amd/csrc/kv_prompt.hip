@@ -11,14 +11,16 @@
 //   * sums: values as the first operand, 32 channels of a row in a lane's 16 accumulators.
 // Rounding code * scale to fp16 (2^-11) is below a bf16 output's own rounding but twice an fp16
 // output's, since scores feel it; with PREC (fp16 and fp32 outputs) the exact remainder of every
-// key and value is kept beside it and enters by a second product: rms error 2.2e-4 .. 2.8e-4, where
-// values without theirs give 2.8e-4 .. 3.4e-4 in 992 instead of 1255 us (three chunks of 2048 rows
-// behind 6144 keys, 32 / 8 heads of 128).
+// key and value is kept beside it and enters by a second product: rms error 2.2e-4 .. 2.8e-4 (without the
+// values' remainder 2.8e-4 .. 3.4e-4 in four fifths of the time).  fp32 queries round to 11 bits as in the
+// other kernel: behind int8 rows their own error is 2^-8, and a second part of the query would double
+// the scores' products once more.
 //
 // Bound: MFMA and the softmax's VALU, about even at 128 channels (a wave's turn of 64 keys: 32 products of
 // 32 cycles, some 230 VALU of 4 and more) and hardly overlapping between the two waves of a SIMD:
-// three chunks of 2048 rows behind 6144 keys, 32 / 8 heads of 128, run at 940 TFLOP/s (a large
-// library product: 1206), unlike ones (1024 .. 2048 rows of 8192 and fewer) at 850 to 890.
+// three chunks of 2048 rows behind 6144 keys, 32 / 8 heads of 128, take 781 us in bf16, 924 TFLOP/s (a
+// large library product: 1206), and 1207 us in fp16; unlike chunks in bf16 (1024 .. 2048 rows of 8192 tokens and
+// fewer) run at 830 to 860 TFLOP/s.
 #include "kv_attention.h"
 
 namespace q4gsw {

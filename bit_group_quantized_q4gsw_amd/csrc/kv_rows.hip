@@ -22,7 +22,7 @@
 // second launch (kv_join_kernel).
 //
 // Bound: HBM for long caches (36 * dim bytes per 32 tokens and head): 64 sequences of 4096 .. 16384
-// tokens, 8 heads of 128, 719 MB in 150 us, 4.8 TB/s (a large copy: 4.72).  At 128 channels a unit
+// tokens, 8 heads of 128, 719 MB in 152 us, 4.7 TB/s (a large copy: 4.72).  At 128 channels a unit
 // costs some 290 VALU and 16 products a wave, two thirds of the time its bytes take.  Short caches are
 // latency: 3 us to the first unit, 2 us for the waves' join, 4 to 5 us for the splits' join.
 #include "kv_attention.h"

@@ -90,14 +90,13 @@ void finish_plan(AttnPlan& p, const AttnSize& n, int64_t splits) {
     p.us = p.splits > 1 ? 3.0f + 2e-6f * p.splits * n.batch * n.heads * n.rows * n.dim : 0.0f;
 }
 
-// Few rows.  The splits of the keys fill the workgroups that fit the GPU at once (32 sequences of
-// 1024 .. 4096 tokens, 8 heads of 128: 3 splits 31.5 us, 8 splits 34.7; two of 131072: 48 splits 58
-// us, 192 splits 73), but a split has 8 blocks, and 16 blocks are not split at all: the join's
-// launch costs more (509 tokens, heads of 64: 6.6 us, 2 splits 8.5; four of 1024, heads of 128: 10.9 us,
-// 4 splits 9.4).  Where that leaves long
-// splits and few turns, unlike lengths end at unlike times, and shorter splits balance them (64
-// sequences of 4096 .. 16384: 1 split 209 us, 8 splits 151).  Eight waves serve a grid of at most
-// a workgroup per CU (509 tokens: 6.6 us against 7.1; 1024 workgroups of 512 tokens: 15.4 against 11.6).
+// Few rows.  The splits of the keys fill the workgroups that fit the GPU at once (us, single tokens of 32 / 8
+// heads of 128; 32 sequences of 1024 .. 4096 tokens, fp16: 3 splits 33, 1 split 38, 8 splits 34; two of 131072, bf16: 48
+// splits 62, 192 splits 75), but a split has 8 blocks, and 16 blocks are not split at all: the join's
+// launch costs more (509 tokens, heads of 64: 7.1, 2 splits 8.5; four of 1024: 11.7, 4 splits 9.7).  Where that leaves
+// long splits and few turns, unlike lengths end at unlike times, and shorter splits balance them (64
+// sequences of 4096 .. 16384: 1 split 207, 8 splits 171).  Eight waves serve a grid of at most a
+// workgroup per CU (509 tokens: 7.1 against 7.7; 1024 workgroups of 512 tokens: 31.7 against 21.9).
 // The estimate: time of a tile of 16 rows by 32 keys on a CU, of which a grid that fits at once gives the
 // fullest CU a whole number, and of a workgroup's loads and join.
 AttnPlan plan_rows(const AttnSize& n) {
