@@ -57,6 +57,13 @@ q4gsw_status check_seqs(const q4gsw_kv_seqs* s, KvSeqs* v) {
     return Q4GSW_OK;
 }
 
+// Does an output overlap the arrays that describe the sequences?
+bool over_seqs(const KvSeqs& s, Range out) {
+    const uint64_t table = s.table_cols ? ((uint64_t)(s.batch - 1) * s.table_ld + s.table_cols) * 4 : 0;
+    return overlap(out, range_of(s.table, table)) || overlap(out, range_of(s.cu, (uint64_t)(s.batch + 1) * 4)) ||
+           overlap(out, range_of(s.lens, (uint64_t)s.batch * 4));
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Bytes of token rows `ld` elements apart, the last one `row` elements long.
@@ -267,7 +274,7 @@ q4gsw_status q4gsw_kv_append(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s, co
     const int es = esize(dtype);
     if (!aligned16(k) || !aligned16(v) || (k_ld * es) % 16 != 0 || (v_ld * es) % 16 != 0) return Q4GSW_E_ALIGN;
     if (overlap(cr, range_of(k, rows_extent(sv.tokens, k_ld, row, es))) ||
-        overlap(cr, range_of(v, rows_extent(sv.tokens, v_ld, row, es))))
+        overlap(cr, range_of(v, rows_extent(sv.tokens, v_ld, row, es))) || over_seqs(sv, cr))
         return Q4GSW_E_ALIAS;
     return hip_status(launch_kv_append(cv, sv, k, k_ld, v, v_ld, dtype, static_cast<hipStream_t>(stream)));
 }
@@ -284,7 +291,7 @@ q4gsw_status q4gsw_kv_read(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s, floa
     if (!aligned16(k) || !aligned16(v)) return Q4GSW_E_ALIGN;
     const uint64_t n = (uint64_t)sv.tokens * cv.heads * cv.dim * 4;
     const Range kr = range_of(k, n), vr = range_of(v, n);
-    if (overlap(kr, vr) || overlap(kr, cr) || overlap(vr, cr)) return Q4GSW_E_ALIAS;
+    if (overlap(kr, vr) || overlap(kr, cr) || overlap(vr, cr) || over_seqs(sv, kr) || over_seqs(sv, vr)) return Q4GSW_E_ALIAS;
     return hip_status(launch_kv_read(cv, sv, k, v, static_cast<hipStream_t>(stream)));
 }
 
@@ -358,7 +365,8 @@ q4gsw_status q4gsw_kv_attention_ex(const q4gsw_kv_cache* c, const q4gsw_kv_seqs*
     if (!ws_ok(ws, ws_bytes, need)) return Q4GSW_E_WORKSPACE;
     const Range qr = range_of(q, rows_extent(s->tokens, q_ld, row, es));
     const Range orr = range_of(out, (uint64_t)s->tokens * row * es), sr = range_of(ws, need);
-    if (overlap(orr, qr) || overlap(orr, cr) || overlap(sr, orr) || overlap(sr, qr) || overlap(sr, cr))
+    if (overlap(orr, qr) || overlap(orr, cr) || overlap(sr, orr) || overlap(sr, qr) || overlap(sr, cr) ||
+        over_seqs(a.sq, orr) || over_seqs(a.sq, sr))
         return Q4GSW_E_ALIAS;
     a.q = q;
     a.q_ld = q_ld;

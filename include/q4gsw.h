@@ -479,7 +479,7 @@ q4gsw_status q4gsw_kv_read(const q4gsw_kv_cache *c, const q4gsw_kv_seqs *s, floa
  * order its sums otherwise.  Tokens of 0 launch nothing.
  * E_NULL, E_SHAPE (hq not a multiple of heads; sizes, a launch of 2^32 threads among them; window negative;
  * softcap neither 0 nor in 1e-30..1e30),
- * E_DTYPE, E_BUFFER, E_ALIGN, E_WORKSPACE, E_ALIAS (out or ws overlaps q, the cache or each other).
+ * E_DTYPE, E_BUFFER, E_ALIGN, E_WORKSPACE, E_ALIAS (out or ws overlaps an input, the cache or each other).
  */
 q4gsw_status q4gsw_kv_attention_workspace_bytes(const q4gsw_kv_cache *c, int32_t batch, int64_t tokens, int32_t hq,
                                                 int32_t max_new, int32_t max_ctx, uint64_t *bytes);
