@@ -278,3 +278,32 @@ def test_joins_of_few_and_many_splits(dim, dtype, length):
     sharp(want, bound, expected(x, [k.roll(1, 0) for k in keys], values, lens, news)[0], part=0.8)
     got = q.kv_attention(cache, x.cuda(), table, offsets(news), ln, 2, length)
     check(got, want, bound, f"{splits} splits", 2 * rms_limit(dtype))
+
+
+@pytest.mark.parametrize("dim,dtype", [(128, BF16), (256, F16)])
+def test_pages_past_4_gib(dim, dtype):
+    """Pages whose bytes lie past 2^32 from the cache's start: append, read-out and both kernels."""
+    q = lib()
+    page, heads, length, new, hq = 64, 8, 500, 40, 8
+    pages = (5 << 30) // (36 * dim * heads * (page // 32))
+    print(f"far pages dim={dim} {dtype} {pages} pages", flush=True)
+    cache = q.kv_cache(pages, page, heads, dim)
+    need = -(-length // page)
+    first = pages - need
+    assert cache.buffer.numel() * first // pages > 1 << 32
+    table = (first + torch.randperm(need, generator=torch.Generator().manual_seed(2))).int().view(1, need).cuda()
+    gen = torch.Generator().manual_seed(dim)
+    k = (STEP * whole_keys(length, heads, dim, gen)).to(dtype)
+    v = torch.randn(length, heads, dim, generator=gen).to(dtype)
+    ln = torch.tensor([length], dtype=torch.int32, device="cuda")
+    q.kv_append(cache, k.cuda(), v.cuda(), table, offsets([length]), ln)
+    rk, rv = q.kv_read(cache, table, offsets([length]), ln, length)
+    assert torch.equal(rk.cpu().double(), kv_values(k)) and torch.equal(rv.cpu().double(), kv_values(v))
+    assert not cache.buffer[:cache.buffer.numel() // pages * first].any()
+    x = torch.randint(-4, 5, (new, hq, dim), generator=gen).to(dtype)
+    want, bound = expected(x, [kv_values(k)], [kv_values(v)], [length], [new])
+    sharp(want, bound)
+    for kernel in KERNELS:
+        with q.forced_kv_kernel(kernel):
+            got = q.kv_attention(cache, x.cuda(), table, offsets([new]), ln, new, length)
+        check(got, want, bound, kernel)
