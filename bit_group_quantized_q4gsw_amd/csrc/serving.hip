@@ -81,20 +81,31 @@ struct AttnPlan {
 
 struct AttnSize {
     int heads, dim, batch, rows; // rows: new tokens times query heads of a cache head
-    int64_t blocks;              // of 32 keys that some row may see
-    float mean;                  // of them that a row sees
+    int group, max_new, max_ctx, window;
+    float mean;                  // blocks of 32 keys that a row sees
     bool prec;                   // kv_prompt keeps the remainders of keys and values
+
+    // Blocks that some tile of `tile` rows may see: behind a window those of the window and of the
+    // tile's own tokens, and its first row's window may begin and its last row's end inside a block.
+    int64_t blocks(int tile) const {
+        int64_t span = max_ctx;
+        if (window) {
+            const int64_t own = (tile - 2) / group + 2, seen = window + (own < max_new ? own : max_new) + 30;
+            span = seen < span ? seen : span;
+        }
+        return (span + kKvTok - 1) / kKvTok;
+    }
 };
 
 constexpr int kCus = 256;
 constexpr int kFewRows = 32;     // never the kernel of many rows
 
-void finish_plan(AttnPlan& p, const AttnSize& n, int64_t splits) {
+void finish_plan(AttnPlan& p, const AttnSize& n, int64_t blocks, int64_t splits) {
     p.splits = (int)(splits < 1 ? 1 : splits);
-    p.chunk = (int)((n.blocks + p.splits - 1) / p.splits);
+    p.chunk = (int)((blocks + p.splits - 1) / p.splits);
     p.chunk += p.chunk & 1;
-    // the join: its launch, and the partials written and read at some 4 TB/s
-    p.us = p.splits > 1 ? 3.0f + 2e-6f * p.splits * n.batch * n.heads * n.rows * n.dim : 0.0f;
+    // the join: its launch, and the partials written and read at some 5 TB/s
+    p.us = p.splits > 1 ? 3.0f + 1.6e-6f * p.splits * n.batch * n.heads * n.rows * n.dim : 0.0f;
 }
 
 // Few rows.  The splits of the keys fill the workgroups that fit the GPU at once (us, single tokens of 32 / 8
@@ -110,17 +121,18 @@ AttnPlan plan_rows(const AttnSize& n) {
     AttnPlan p{};
     p.row_tiles = (n.rows + 15) / 16;
     const int64_t groups = (int64_t)n.batch * n.heads * p.row_tiles, fit = kCus * kv_rows_waves(n.dim);
+    const int64_t blocks = n.blocks(16);
     int64_t splits = 1;
-    if (n.blocks > 16) {
-        splits = fit / groups < n.blocks / 8 ? fit / groups : n.blocks / 8;
+    if (blocks > 16) {
+        splits = fit / groups < blocks / 8 ? fit / groups : blocks / 8;
         if (splits < 1) splits = 1;
-        if (n.blocks > 96 * splits && groups < 4 * fit) splits = (n.blocks + 63) / 64;
+        if (blocks > 96 * splits && groups < 4 * fit) splits = (blocks + 63) / 64;
     }
-    finish_plan(p, n, splits);
+    finish_plan(p, n, blocks, splits);
     p.waves = groups * p.splits <= kCus ? 8 : 4;
     const float turns = (float)groups * p.splits / fit;
     const float per_cu = turns <= 1 ? (float)((groups * p.splits + kCus - 1) / kCus) : (float)groups * p.splits / kCus;
-    p.us += 4.0f + (0.085f + 0.0045f * n.dim) * per_cu * n.mean / (4 * p.splits) + (2.0f + 0.026f * n.dim) * (turns < 1 ? 1 : turns);
+    p.us += 2.5f + (0.09f + 0.0048f * n.dim) * per_cu * n.mean / (4 * p.splits) + (2.0f + 0.026f * n.dim) * (turns < 1 ? 1 : turns);
     return p;
 }
 
@@ -136,13 +148,14 @@ float prompt_turn(int dim, bool prec) {
 // 2 splits 106; 1024 behind 7000, 128 workgroups: 2 splits 161 us, 1 split 237, 3 splits 198).
 int64_t prompt_splits(const AttnSize& n, int waves, bool prec) {
     const int64_t groups = (int64_t)n.batch * n.heads * ((n.rows + 32 * waves - 1) / (32 * waves));
-    const int64_t fill = kCus * prompt_fit(n.dim, prec, waves) / groups, most = (n.blocks + 15) / 16;
+    const int64_t fill = kCus * prompt_fit(n.dim, prec, waves) / groups, most = (n.blocks(32 * waves) + 15) / 16;
     const int64_t splits = fill < most ? fill : most;
     return splits < 1 ? 1 : splits;
 }
 
 // Many rows: eight waves (up to 128 channels), which share a tile's unpacking, or four, and keys split as far
-// as the grid fits or not at all, by the estimate: a workgroup's own turns, or all turns over the CUs.  Of workgroups of
+// as the grid fits or not at all, by the estimate: a workgroup's loads and end each time that one starts on a
+// CU, and its own turns, or all turns over the CUs.  Of workgroups of
 // four waves that fit a CU twice two take 1.3 times the turn of one of eight waves, and one alone 0.85 times.  Prompts
 // from their beginning have rows of unlike lengths, which splits balance badly (1024 tokens, 32 / 8 heads of 128, bf16: four
 // waves 37.5 us, 2 splits 47; eight waves 41 and 45); few rows need them (256 tokens behind 3744: eight waves
@@ -158,13 +171,15 @@ AttnPlan plan_prompt(const AttnSize& n) {
         const int fit = prompt_fit(n.dim, n.prec, waves);
         const bool half = waves == 4 && n.dim <= 128;
         for (int64_t splits = 1;; splits = most) {
-            finish_plan(p, n, splits);
-            float turns = (float)groups * p.splits / (kCus * fit);
-            const float whole = 0.9f * ((groups * p.splits + kCus * fit - 1) / (kCus * fit));
-            if (fit == 1 && turns < whole) turns = whole;            // a last turn that fills few CUs
+            finish_plan(p, n, n.blocks(32 * waves), splits);
+            float turns = (float)groups * p.splits / (kCus * fit), starts = turns < 1 ? 1 : turns;
+            if (fit == 1) {                                          // a last turn may fill few CUs
+                starts = (float)((groups * p.splits + kCus - 1) / kCus);
+                turns = turns < 0.9f * starts ? 0.9f * starts : turns;
+            }
             const float all = (half ? (fit == 2 ? 1.3f : 0.85f) : 1.0f) * turns * 0.5f * n.mean / p.splits;
             const float longest = (half ? 0.85f : 1.0f) * 0.5f * p.chunk;
-            p.us += 6.0f + prompt_turn(n.dim, n.prec) * (longest > all ? longest : all);
+            p.us += (4.6f + 0.026f * n.dim) * starts + prompt_turn(n.dim, n.prec) * (longest > all ? longest : all);
             if (best.waves == 0 || p.us < best.us) best = p;
             if (splits >= most) break;
         }
@@ -173,17 +188,9 @@ AttnPlan plan_prompt(const AttnSize& n) {
 }
 
 AttnSize attention_size(int heads, int dim, int batch, int hq, int max_new, int max_ctx, int window, int dtype) {
-    AttnSize n{heads, dim, batch, max_new * (hq / heads), 0, 0.0f, dtype != kBF16};
-    int64_t span = max_ctx;
     float mean = max_ctx > max_new ? max_ctx - 0.5f * max_new : 0.5f * max_ctx;
-    if (window) {
-        // the first row's window may begin and the last row's end inside a block
-        if (window + (int64_t)max_new + 30 < span) span = window + (int64_t)max_new + 30;
-        if (window + 32.0f < mean) mean = window + 32.0f;
-    }
-    n.blocks = (span + kKvTok - 1) / kKvTok;
-    n.mean = mean / kKvTok;
-    return n;
+    if (window && window + 32.0f < mean) mean = window + 32.0f;
+    return AttnSize{heads, dim, batch, max_new * (hq / heads), hq / heads, max_new, max_ctx, window, mean / kKvTok, dtype != kBF16};
 }
 
 // Many rows share a tile's unpacking but take 64 keys in turn after turn, few rows spread over the GPU;
@@ -191,7 +198,8 @@ AttnSize attention_size(int heads, int dim, int batch, int hq, int max_new, int 
 // from their beginning of 32 / 8 heads of 128: 512 tokens 19 / 23 (18 / 27), 1024 tokens 42 / 38 (42 / 48), 2048 tokens
 // 118 / 71 (119 / 97), two of 2048 tokens 223 / 98 (219 / 137); 1024 tokens behind 7000 377 / 161 (372 / 234); of 16 / 4 heads
 // of 256: 2048 tokens 129 / 127 (130 / 198), two of 2048 tokens 235 / 152 (231 / 234), three chunks of 2048 behind 6144
-// 1732 / 1262 (1735 / 2026).  Up to 32 rows never fill the workgroup of many.
+// 1732 / 1262 (1735 / 2026).  Of 378 prompts, chunks and drafts of random sizes, 104 of
+// them windowed, it takes the slower kernel by over 10% for 12, by 31% at most.  Up to 32 rows never fill the workgroup of many.
 AttnPlan plan_attention(const AttnSize& n, int kernel) {
     if (kernel == Q4GSW_KV_MANY_ROWS) return plan_prompt(n);
     const AttnPlan few = plan_rows(n);

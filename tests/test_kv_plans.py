@@ -70,7 +70,37 @@ MEASURED = [
 ]
 
 
-@pytest.mark.parametrize("case", MEASURED, ids=lambda c: "-".join(map(str, c[:7])))
+# drafts and short prompts: a turn of the kernel of many rows costs more than they have to do
+SHORT = [
+    (128, 8, 2, 2, 6, 14, 14, 7.5, 9.4),
+    (96, 16, 4, 2, 1, 28, 28, 7.2, 8.5),
+    (128, 32, 4, 1, 1, 21, 51, 7.7, 10.7),
+    (256, 48, 8, 2, 2, 32, 32, 11.3, 16.2),
+    (192, 6, 1, 1, 2, 38, 38, 9.3, 14.7),
+    (64, 16, 4, 2, 7, 59, 59, 6.9, 8.1),
+    (192, 16, 8, 1, 3, 47, 47, 9.6, 14.1),
+    (64, 1, 1, 2, 2, 43, 51, 6.2, 7.2),
+]
+# windows: a workgroup sees the window and its own tokens, not all of the prompt's
+WINDOWS = [
+    (64, 32, 4, 2, 1, 2370, 2370, 48.7, 25.2, 421),
+    (128, 32, 8, 2, 1, 1764, 3901, 47.7, 26.1, 224),
+    (128, 8, 2, 2, 3, 1656, 1656, 32.0, 22.3, 180),
+    (256, 64, 8, 1, 1, 1169, 1170, 116.4, 95.7, 183),
+]
+
+
+@pytest.mark.parametrize("case", MEASURED + SHORT + WINDOWS, ids=lambda c: "-".join(map(str, c[:7])))
 def test_the_faster_kernel_is_taken(q, case):  # noqa: F811
-    few, many = case[7:]
-    assert plan(q, *case[:7]).kernel == (1 if few < many else 2)
+    few, many, *window = case[7:]
+    assert plan(q, *case[:7], 0, *window).kernel == (1 if few < many else 2)
+
+
+@pytest.mark.parametrize("kernel", [1, 2])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_splits_of_a_window(q, dim, kernel):  # noqa: F811
+    """Rows behind a window are split as the same rows behind that many keys, whatever the prompt's length."""
+    for window, new, ctx in ((200, 3000, 20000), (500, 1000, 1000), (4096, 300, 60000)):
+        p = plan(q, dim, 4, 1, 2, 1, new, ctx, kernel, window)
+        blocks = (window + 64 * 4 + 62) // 32
+        assert p.splits <= max(1, -(-blocks // (8 if kernel == 1 else 16))), (window, new, ctx)
