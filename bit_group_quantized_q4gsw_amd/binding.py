@@ -158,6 +158,10 @@ def lib() -> ctypes.CDLL:
             "q4gsw_kv_attention_plan": [pc, i32, i64, i32, i32, i32, i32, i32, ko, ctypes.POINTER(KvPlanInfo)],
             "q4gsw_kv_attention": [pc, ps, vp, i64, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, u64, vp],
             "q4gsw_kv_attention_ex": [pc, ps, vp, i64, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, u64, ko, vp],
+            "q4gsw_kv_tree_attention_workspace_bytes": [pc, i32, i64, i32, i32, i32, ctypes.POINTER(u64)],
+            "q4gsw_kv_tree_attention": [pc, ps, vp, vp, i64, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, u64, vp],
+            "q4gsw_kv_tree_attention_ex": [pc, ps, vp, vp, i64, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, u64, ko, vp],
+            "q4gsw_kv_keep": [pc, i32, ps, vp, vp, i32, vp, vp, vp],
             "q4gsw_adapter_workspace_bytes": [i32, pw, i64, i32, i32, ctypes.POINTER(u64)],
             "q4gsw_adapter_fwd": [pw, vp, i32, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, u64, vp],
             "q4gsw_adapter_bwd": [pw, vp, vp, i32, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, vp, vp, u64, vp],
@@ -196,6 +200,15 @@ def _stream() -> int:
     """The current device's current stream as the integer a stream argument takes (through torch's raw
     accessors: building a Stream object costs more than a small kernel's launch)."""
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _stream_of(dev: int) -> int:
+    """The current stream of the device of a call's tensors, which has to be the current device: a kernel is
+    launched there."""
+    current = torch._C._cuda_getDevice()
+    if dev != current:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{current}")
+    return torch._C._cuda_getCurrentRawStream(current)
 
 
 def _dev(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -577,13 +590,29 @@ def kv_attention_plan(cache: KvCache, batch: int, tokens: int, hq: int, max_new:
     return {"kernel": next(k for k, v in KV_KERNELS.items() if v == info.kernel), "waves": info.waves, "splits": info.splits}
 
 
+def _per_row(t: torch.Tensor, n: int, dev: int, name: str) -> torch.Tensor:
+    """`t` itself, or a dense copy: int32 [n] on the device of that index."""
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n or t.get_device() != dev:
+        raise ValueError(f"{name} must be an int32 tensor [{n}] on cuda:{dev}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _int_out(out: Optional[torch.Tensor], shape: Tuple[int, ...], device, name: str) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    if out.dtype is not torch.int32 or tuple(out.shape) != shape or out.device != device or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on {device}")
+    return out
+
+
 def kv_attention(cache: KvCache, q: torch.Tensor, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor,
                  max_new: int, max_ctx: int, window: int = 0, softcap: float = 0.0,
-                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, parents: Optional[torch.Tensor] = None) -> torch.Tensor:
     """out [tokens, hq, dim] of q's dtype: causal attention of the new tokens q over the cache, which
     holds their own keys and values already.  max_new and max_ctx bound the sequences' new tokens and
     lengths; window > 0 keeps the last `window` keys of each token, softcap > 0 caps the scores.  A row that
-    sees no key gives zeros, else one whose query holds a NaN or an infinity gives NaN."""
+    sees no key gives zeros, else one whose query holds a NaN or an infinity gives NaN.  With `parents` the new tokens form a tree
+    (kv_tree_attention)."""
     if (max_new | max_ctx | window) >> 31:       # negative ones too, of which the library refuses the 32-bit ones
         _int32(max_new, max_ctx, window)
     if q.dim() != 3:
@@ -597,15 +626,77 @@ def kv_attention(cache: KvCache, q: torch.Tensor, table: torch.Tensor, cu: torch
     elif out.dtype is not dt or out.shape != shape or out.get_device() != cache._dev or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {dt} tensor [tokens, hq, dim] on {cache.buffer.device}")
     seqs = _kv_seqs(cache, table, cu, lens, tokens)
+    if parents is not None:
+        parents = _per_row(parents, tokens, cache._dev, "parents")
     if workspace is None:
-        need = kv_attention_workspace_bytes(cache, lens.numel(), tokens, hq, max_new, max_ctx)
+        need = (kv_attention_workspace_bytes if parents is None else kv_tree_attention_workspace_bytes)(
+            cache, lens.numel(), tokens, hq, max_new, max_ctx)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != cache._dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {cache.buffer.device}")
-    _check(lib().q4gsw_kv_attention_ex(cache._ref, seqs, qp, q_ld, code, hq, max_new, max_ctx, window, softcap,
-                                       out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                       _local.kv, _stream()), "q4gsw_kv_attention")
+    if parents is None:
+        _check(lib().q4gsw_kv_attention_ex(cache._ref, seqs, qp, q_ld, code, hq, max_new, max_ctx, window, softcap,
+                                           out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                           _local.kv, _stream()), "q4gsw_kv_attention")
+    else:
+        _check(lib().q4gsw_kv_tree_attention_ex(cache._ref, seqs, parents.data_ptr(), qp, q_ld, code, hq, max_new, max_ctx,
+                                                window, softcap, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                                _local.kv, _stream_of(cache._dev)), "q4gsw_kv_tree_attention")
     return out
+
+
+def kv_tree_attention_workspace_bytes(cache: KvCache, batch: int, tokens: int, hq: int, max_new: int, max_ctx: int) -> int:
+    """Workspace of kv_tree_attention calls with these sizes (any window)."""
+    _int32(batch, hq, max_new, max_ctx)
+    out = ctypes.c_uint64()
+    _check(lib().q4gsw_kv_tree_attention_workspace_bytes(cache._ref, batch, tokens, hq, max_new, max_ctx, ctypes.byref(out)),
+           "q4gsw_kv_tree_attention_workspace_bytes")
+    return out.value
+
+
+def kv_tree_attention(cache: KvCache, q: torch.Tensor, parents: torch.Tensor, table: torch.Tensor, cu: torch.Tensor,
+                      lens: torch.Tensor, max_new: int, max_ctx: int, window: int = 0, softcap: float = 0.0,
+                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """kv_attention of drafted tokens that form a tree: parents (int32 [tokens]) of the row of a sequence's
+    node i is its parent's number in the sequence's new tokens, below i; any other value makes it a root.
+    A node sees the tokens before the tree, its ancestors and itself; with window > 0 those whose position
+    is above its own - window, a node's position being that of the tree's start + its depth.  max_new is
+    at most 512."""
+    if parents is None:
+        raise ValueError("parents must be given")
+    return kv_attention(cache, q, table, cu, lens, max_new, max_ctx, window, softcap, out, workspace, parents)
+
+
+def kv_keep(caches, parents: torch.Tensor, leaf: torch.Tensor, table: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor,
+            max_new: int, kept: Optional[torch.Tensor] = None,
+            path: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(kept, path) int32 [batch], [batch, max_new]: the nodes on the way from a root of sequence b's tree to
+    node leaf[b] (int32 [batch]; outside the tree: none) move to the places behind the tokens before the tree,
+    in `caches` (a KvCache, or a sequence of up to 128 of one shape that share the table).  kept: the tokens
+    that each sequence has then; path: the nodes moved, in order, then -1."""
+    caches = (caches,) if isinstance(caches, KvCache) else tuple(caches)
+    if not caches:
+        raise ValueError("caches must hold at least one cache")
+    first = caches[0]
+    for c in caches:
+        if c._dev != first._dev:
+            raise ValueError("caches must be on one device")
+    _int32(max_new)
+    if max_new < 1:
+        raise ValueError("max_new must be positive")
+    if parents.dim() != 1:
+        raise ValueError("parents must be an int32 tensor [tokens]")
+    tokens = parents.numel()
+    parents = _per_row(parents, tokens, first._dev, "parents")
+    seqs = _kv_seqs(first, table, cu, lens, tokens)
+    B = lens.numel()
+    leaf = _per_row(leaf, B, first._dev, "leaf")
+    dev = first.buffer.device
+    kept, path = _int_out(kept, (B,), dev, "kept"), _int_out(path, (B, max_new), dev, "path")
+    descs = first._ref if len(caches) == 1 else (KvCacheDesc * len(caches))(*[c.desc for c in caches])
+    _check(lib().q4gsw_kv_keep(descs, len(caches), seqs, parents.data_ptr(), leaf.data_ptr(), max_new, kept.data_ptr(),
+                               path.data_ptr(), _stream_of(first._dev)), "q4gsw_kv_keep")
+    return kept, path
 
 
 def adapter_workspace_bytes(op: int, w: PackedWeight, M: int, dtype: torch.dtype, rank: int) -> int:

@@ -175,6 +175,11 @@ struct KvSeqs;
 hipError_t launch_kv_append(const KvView& c, const KvSeqs& sq, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
                             int dtype, hipStream_t s);
 hipError_t launch_kv_read(const KvView& c, const KvSeqs& sq, float* k, float* v, hipStream_t s);
+// The path to node leaf[b] of each sequence's tree moved together behind the tokens before the tree, in up
+// to kKeepCaches caches alike but for their data; kept and path (may be null) written once.
+constexpr int kKeepCaches = 128;
+hipError_t launch_kv_keep(const KvView* caches, int count, const KvSeqs& sq, const int32_t* parents, const int32_t* leaf,
+                          int max_new, int32_t* kept, int32_t* path, hipStream_t s);
 
 // adapter.hip: the low-rank adapter terms beside the frozen weight (rank 1..adapter_rank_max())
 // and the AdamW update.  The forward writes t = x A^T [M, r], then y += alpha t B^T; its

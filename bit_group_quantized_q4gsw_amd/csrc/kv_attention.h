@@ -1,6 +1,6 @@
 // Shared by the attention kernels over the 4-bit cache (kv_rows.hip, kv_prompt.hip).
 #pragma once
-#include "kv4.h"
+#include "kv_tree.h"
 
 namespace q4gsw {
 
@@ -20,6 +20,8 @@ struct KvAttnArgs {
     float scale;             // dim^-1/2
     int splits, chunk;       // blocks of 32 tokens per split (the last split takes the rest)
     int row_tiles;
+    const int32_t* parents;  // trees: of every token row, in its sequence's count of new tokens
+    int tree_at;             // their place in the workgroup's LDS
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -37,15 +39,17 @@ __device__ __forceinline__ int kv_left_behind(const KvAttnArgs& a, int place) {
 }
 
 // What the rows [r0, r0 + nr) of one (sequence, cache head) see: row r is new token r / group,
-// query head r % group; its place is p0 + r / group.
+// query head r % group; its place is p0 + r / group, and so is its position but in a tree, where it may be
+// any from p0 on.
 struct KvSpan {
-    int pmin, pmax;          // places of the first and last row
+    int pmin, pmax;          // places of the first and last row (pmin: the lowest position)
     int64_t lo, hi;          // 32-token blocks [lo, hi) of this split
 };
+template <bool TREE = false>
 __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs& a, const KvSeq& s, int r0, int nr, int split) {
     KvSpan r;
     const int p0 = s.len - s.m;
-    r.pmin = p0 + r0 / a.group;
+    r.pmin = TREE ? p0 : p0 + r0 / a.group;
     r.pmax = p0 + (r0 + nr - 1) / a.group;
     int64_t first = a.window ? (int64_t)r.pmin - a.window + 1 : 0;
     first = first < 0 ? 0 : first;
@@ -171,6 +175,11 @@ constexpr int prompt_lds(int D, bool prec) { return 2 * prompt_blocks(D, prec) *
 constexpr int prompt_fit(int D, bool prec, int waves) {
     const int by_regs = (D <= 128 ? 8 : 4) / waves, by_lds = 160 * 1024 / prompt_lds(D, prec);
     return by_regs < by_lds ? by_regs : by_lds;
+}
+
+// Bytes of the trees' part of a workgroup's LDS, for tiles of `rows` rows; a call without trees has none.
+inline int tree_lds(const KvAttnArgs& a, int rows) {
+    return a.parents ? tree_bytes(a.max_new, tree_tokens(rows, a.group, a.max_new)) : 0;
 }
 
 // kv_rows.hip: `waves` (4 or 8) per workgroup, tiles of 16 rows.

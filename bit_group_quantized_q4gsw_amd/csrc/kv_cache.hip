@@ -17,7 +17,7 @@
 // 15 of it the codes' VALU (two IEEE divisions an octet, eight steps an element).  Single tokens take 6
 // and 4 us, which is three rounds of loads.
 #include "internal.h"
-#include "kv4.h"
+#include "kv_tree.h"
 
 namespace q4gsw {
 namespace {
@@ -96,6 +96,57 @@ __device__ __forceinline__ int to_int(float v) {
     return r;
 }
 
+// 24 bytes more a token: the four tokens that a wave gathers at once lie in other banks
+template <int D>
+constexpr int kVcRow = D + 24;
+
+// The whole workgroup: tokens [t0, t1) of a unit, from keys' words in plane order, values' codes
+// [token][channel] and scales in layout order in LDS.
+template <int D>
+__device__ __forceinline__ void store_block(uint8_t* unit, int t0, int t1, const uint32_t* s_kw, const uint8_t* s_vc,
+                                            const uint16_t* s_ksc, const uint16_t* s_vsc) {
+    constexpr int G = D / 32;
+    const int tid = threadIdx.x;
+    // words of one plane in address order: lane and word of 4-byte place n
+    auto place = [](int n, int& w, int& lane) {
+        const int p = n >> 8;
+        if ((G & 1) && p == G / 2) {
+            lane = (n & 255) >> 1;
+            w = 4 * p + (n & 1);
+        } else {
+            lane = (n & 255) >> 2;
+            w = 4 * p + (n & 3);
+        }
+    };
+    uint32_t* kw = reinterpret_cast<uint32_t*>(unit);
+    uint32_t* vw = reinterpret_cast<uint32_t*>(unit + 512 * G);
+    uint16_t* ksc = reinterpret_cast<uint16_t*>(unit + 1024 * G);
+    uint16_t* vsc = ksc + 32 * G;
+    for (int n = tid; n < 128 * G; n += kThreads) {
+        int w, lane;
+        place(n, w, lane);
+        const int i = lane & 15, q = lane >> 4;
+        const int t = kv_tok(i >> 2, 4 * (w & 1) + (i & 3));
+        if (t >= t0 && t < t1) kw[n] = s_kw[n];
+        uint32_t word = 0, mask = 0;
+#pragma unroll
+        for (int slot = 0; slot < 8; ++slot) {
+            const int tt = kv_tok(q, slot);
+            if (tt < t0 || tt >= t1) continue;
+            word |= (uint32_t)s_vc[tt * kVcRow<D> + 16 * w + i] << (4 * nib_pos(slot));
+            mask |= 0xFu << (4 * nib_pos(slot));
+        }
+        if (mask == 0xFFFFFFFFu) vw[n] = word;
+        else if (mask) vw[n] = (vw[n] & ~mask) | word;
+    }
+    for (int n = tid; n < 32 * G; n += kThreads) {
+        const int t = kv_tok(n / (8 * G), n & 7);
+        if (t < t0 || t >= t1) continue;
+        ksc[n] = s_ksc[n];
+        vsc[n] = s_vsc[n];
+    }
+}
+
 // Four lanes hold the 32 channels of a scale, 8 each.  The arithmetic follows the definition step
 // by step, IEEE division included, so the codes are the definition's bit for bit.  Each item (a
 // token's k-octet) is one coalesced 16-byte load; the codes go through LDS because a word of
@@ -104,10 +155,8 @@ template <int XT, int D>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvView c, KvSeqs sq, const void* __restrict__ k, int64_t k_ld,
                                                              const void* __restrict__ v, int64_t v_ld) {
     constexpr int G = D / 32, kOct = D / 8, kItems = 32 * kOct;
-    // 24 bytes more a token: the four tokens that a wave gathers at once lie in other banks
-    constexpr int kVcRow = D + 24;
     __shared__ uint32_t s_kw[128 * G];                     // keys' words in plane order
-    __shared__ __attribute__((aligned(16))) uint8_t s_vc[32 * kVcRow];    // values' codes [token][channel]
+    __shared__ __attribute__((aligned(16))) uint8_t s_vc[32 * kVcRow<D>];    // values' codes [token][channel]
     __shared__ uint16_t s_sc[2][32 * G];                   // scales in layout order
     const int tid = threadIdx.x, head = blockIdx.y;
     const BlockAt at = find_block(c, sq, blockIdx.x);
@@ -155,7 +204,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvView c, KvSeqs sq
                 u2 w = {0u, 0u};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e >> 2] |= code[e] << (8 * (e & 3));
-                *reinterpret_cast<u2*>(&s_vc[t * kVcRow + 8 * o]) = w;
+                *reinterpret_cast<u2*>(&s_vc[t * kVcRow<D> + 8 * o]) = w;
             }
             if ((o & 3) == 0) s_sc[kv][(q * G + g) * 8 + slot] = bitcast<uint16_t>(sh);
         }
@@ -164,44 +213,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvView c, KvSeqs sq
     uint8_t* const unit = at.unit(c, head);
     if (!unit) return;
 
-    // words of one plane in address order: lane and word of 4-byte place n
-    auto place = [](int n, int& w, int& lane) {
-        const int p = n >> 8;
-        if ((G & 1) && p == G / 2) {
-            lane = (n & 255) >> 1;
-            w = 4 * p + (n & 1);
-        } else {
-            lane = (n & 255) >> 2;
-            w = 4 * p + (n & 3);
-        }
-    };
-    uint32_t* kw = reinterpret_cast<uint32_t*>(unit);
-    uint32_t* vw = reinterpret_cast<uint32_t*>(unit + 512 * G);
-    uint16_t* ksc = reinterpret_cast<uint16_t*>(unit + 1024 * G);
-    uint16_t* vsc = ksc + 32 * G;
-    for (int n = tid; n < 128 * G; n += kThreads) {
-        int w, lane;
-        place(n, w, lane);
-        const int i = lane & 15, q = lane >> 4;
-        const int t = kv_tok(i >> 2, 4 * (w & 1) + (i & 3));
-        if (t >= at.t0 && t < at.t1) kw[n] = s_kw[n];
-        uint32_t word = 0, mask = 0;
-#pragma unroll
-        for (int slot = 0; slot < 8; ++slot) {
-            const int tt = kv_tok(q, slot);
-            if (tt < at.t0 || tt >= at.t1) continue;
-            word |= (uint32_t)s_vc[tt * kVcRow + 16 * w + i] << (4 * nib_pos(slot));
-            mask |= 0xFu << (4 * nib_pos(slot));
-        }
-        if (mask == 0xFFFFFFFFu) vw[n] = word;
-        else if (mask) vw[n] = (vw[n] & ~mask) | word;
-    }
-    for (int n = tid; n < 32 * G; n += kThreads) {
-        const int t = kv_tok(n / (8 * G), n & 7);
-        if (t < at.t0 || t >= at.t1) continue;
-        ksc[n] = s_sc[0][n];
-        vsc[n] = s_sc[1][n];
-    }
+    store_block<D>(unit, at.t0, at.t1, s_kw, s_vc, s_sc[0], s_sc[1]);
 }
 
 // The new tokens' rows back as fp32: value * scale, exact (4 + 11 bits).  A token whose place has
@@ -253,6 +265,104 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvView c, KvSeqs sq, 
     }
 }
 
+// The accepted path of each tree in a row: the nodes on the way from a root to leaf[b] (kv_tree.h) move, as
+// they are, to places p0, p0 + 1, ... behind the p0 tokens before the tree.  One workgroup per (sequence,
+// head) and cache.  Node numbers rise along the path, so the k-th node's place is p0 + k or later: block
+// after block of destinations is gathered into LDS and then stored as the append stores one, and what a
+// block still has to read lies behind all that is written so far.  Nodes in place already are skipped.
+//
+// Bound: latency: the climb, then per block a page number, the codes, and the merge of values' words.
+struct KeepArgs {
+    uint8_t* data[kKeepCaches];
+    KvView c;                            // of every cache, but for the data
+    KvSeqs sq;
+    const int32_t* parents;
+    const int32_t* leaf;
+    int max_new;
+    int32_t* kept;
+    int32_t* path;                       // may be null
+};
+
+template <int D>
+__global__ __launch_bounds__(kThreads) void kv_keep_kernel(KeepArgs a) {
+    constexpr int G = D / 32, kOct = D / 8;
+    __shared__ uint32_t s_kw[128 * G];
+    __shared__ __attribute__((aligned(16))) uint8_t s_vc[32 * kVcRow<D>];
+    __shared__ uint16_t s_sc[2][32 * G];
+    __shared__ int16_t s_up[kTreeMax], s_back[kTreeMax];   // parents, path from the leaf back
+    __shared__ int s_count;
+    const int tid = threadIdx.x, b = blockIdx.x / a.c.heads, head = blockIdx.x % a.c.heads;
+    const KvSeq s = kv_seq(a.sq, b);
+    const int nodes = min(s.m, a.max_new), leaf = a.leaf[b];
+    for (int j = tid; j < nodes; j += kThreads) s_up[j] = tree_parent(a.parents[s.first_row + j], j);
+    __syncthreads();
+    if (tid == 0) {
+        int n = 0;
+        if (leaf >= 0 && leaf < nodes)
+            for (int j = leaf; j >= 0; j = s_up[j]) s_back[n++] = (int16_t)j;
+        s_count = n;
+    }
+    __syncthreads();
+    const int count = s_count;
+    auto node = [&](int k) -> int { return s_back[count - 1 - k]; };
+    const int p0 = s.len - s.m;          // may be negative: such places are none
+    if (blockIdx.y == 0 && head == 0) {
+        if (tid == 0) a.kept[b] = max(p0 + count, 0);
+        if (a.path)
+            for (int k = tid; k < a.max_new; k += kThreads) a.path[(int64_t)b * a.max_new + k] = k < count ? node(k) : -1;
+    }
+    int still = 0;                       // nodes in place: the first ones
+    for (int k0 = 0; k0 < count; k0 += kThreads) still += __syncthreads_count(k0 + tid < count && node(k0 + tid) == k0 + tid);
+    if (still >= count) return;
+
+    KvView c = a.c;
+    c.data = a.data[blockIdx.y];
+    const int sub_mask = (1 << c.bpp_log2) - 1;
+    auto unit_of = [&](int place) -> uint8_t* {
+        const int64_t blk = place >> 5, at = blk >> c.bpp_log2;
+        if (place < 0 || at >= a.sq.table_cols) return nullptr;
+        const int page = a.sq.table[(int64_t)b * a.sq.table_ld + at];
+        return page >= 0 && page < c.pages ? c.data + kv_unit(c, page, head, (int)(blk & sub_mask)) : nullptr;
+    };
+    const int first = max(p0 + still, 0), end = p0 + count;
+    for (int64_t blk = first >> 5; 32 * blk < end; ++blk) {
+        const int base = (int)(32 * blk), t0 = max(first - base, 0), t1 = min(end - base, 32);
+        for (int it = tid; it < 32 * kOct; it += kThreads) {
+            const int t = it / kOct, o = it - t * kOct, g = o >> 2;
+            if (t < t0 || t >= t1) continue;
+            const int from = p0 + node(base + t - p0), ft = from & 31;
+            const uint8_t* src = unit_of(from);
+            const int q = kv_q(t), slot = kv_slot(t), fq = kv_q(ft), fslot = kv_slot(ft);
+            uint32_t key = 0x88888888u;                    // no page there: zeros
+            uint16_t ks = 0, vs = 0;
+            u2 w = {0x08080808u, 0x08080808u};
+            if (src) {
+                key = *reinterpret_cast<const uint32_t*>(src + kv_word_off<G>(2 * g + (fslot >> 2), 16 * (o & 3) + 4 * fq + (fslot & 3)));
+                uint32_t v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int ch = 8 * o + e;
+                    v[e] = *reinterpret_cast<const uint32_t*>(src + 512 * G + kv_word_off<G>(ch >> 4, 16 * fq + (ch & 15)));
+                }
+                ks = reinterpret_cast<const uint16_t*>(src + 1024 * G)[(fq * G + g) * 8 + fslot];
+                vs = reinterpret_cast<const uint16_t*>(src + 1088 * G)[(fq * G + g) * 8 + fslot];
+                w = u2{0u, 0u};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e >> 2] |= ((v[e] >> (4 * nib_pos(fslot))) & 15u) << (8 * (e & 3));
+            }
+            s_kw[kv_word_off<G>(2 * g + (slot >> 2), 16 * (o & 3) + 4 * q + (slot & 3)) >> 2] = key;
+            *reinterpret_cast<u2*>(&s_vc[t * kVcRow<D> + 8 * o]) = w;
+            if ((o & 3) == 0) {
+                s_sc[0][(q * G + g) * 8 + slot] = ks;
+                s_sc[1][(q * G + g) * 8 + slot] = vs;
+            }
+        }
+        __syncthreads();
+        if (uint8_t* const unit = unit_of(base)) store_block<D>(unit, t0, t1, s_kw, s_vc, s_sc[0], s_sc[1]);
+        __syncthreads();
+    }
+}
+
 template <int XT>
 hipError_t append_dims(const KvView& c, const KvSeqs& sq, const void* k, int64_t k_ld, const void* v, int64_t v_ld, dim3 grid,
                        hipStream_t s) {
@@ -299,6 +409,25 @@ hipError_t launch_kv_read(const KvView& c, const KvSeqs& sq, float* k, float* v,
         default: return hipErrorInvalidValue;
     }
 #undef Q4GSW_KV_READ
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_keep(const KvView* caches, int count, const KvSeqs& sq, const int32_t* parents, const int32_t* leaf,
+                          int max_new, int32_t* kept, int32_t* path, hipStream_t s) {
+    KeepArgs a{{}, caches[0], sq, parents, leaf, max_new, kept, path};
+    for (int i = 0; i < count; ++i) a.data[i] = caches[i].data;
+    const dim3 grid((unsigned)(sq.batch * caches[0].heads), (unsigned)count);
+#define Q4GSW_KV_KEEP(D) \
+    case D: hipLaunchKernelGGL((kv_keep_kernel<D>), grid, dim3(kThreads), 0, s, a); break;
+    switch (caches[0].dim) {
+        Q4GSW_KV_KEEP(64)
+        Q4GSW_KV_KEEP(96)
+        Q4GSW_KV_KEEP(128)
+        Q4GSW_KV_KEEP(192)
+        Q4GSW_KV_KEEP(256)
+        default: return hipErrorInvalidValue;
+    }
+#undef Q4GSW_KV_KEEP
     return hipGetLastError();
 }
 

@@ -52,7 +52,7 @@ __device__ __forceinline__ int by_length(const KvSeqs& sq, int rank, int lane) {
     return __builtin_ctzll(__ballot(before == rank));
 }
 
-template <int D, int NW, bool PREC>
+template <int D, int NW, bool PREC, bool TREE>
 __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(KvAttnArgs a) {
     constexpr int G = D / 32, S = D / 16, TB = prompt_blocks(D, PREC);
     constexpr int kFrags = TB * S;                       // operand KBs of the keys (and of the values) of a tile
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
     const int rows = min(s.m, a.max_new) * a.group;
     const int r0 = rt0 * 32 * NW;
     if (r0 >= rows) return;
-    const KvSpan sp = kv_span(a, s, r0, min(32 * NW, rows - r0), split);
+    const KvSpan sp = kv_span<TREE>(a, s, r0, min(32 * NW, rows - r0), split);
     const int64_t nb = sp.hi - sp.lo;
     const int n = nb > 0 ? (int)((nb + TB - 1) / TB) : 0;
 
@@ -88,8 +88,8 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
     const bool ok = r < rows;
     const int tok = ok ? r / a.group : 0, gh = ok ? r - tok * a.group : 0;
     const int p0 = s.len - s.m;
-    const int place = ok ? p0 + tok : sp.pmax;
-    const int wmin = p0 + (r0 + 32 * wave) / a.group;                                   // places of the wave's rows
+    int place = ok ? p0 + tok : sp.pmax;
+    const int wmin = TREE ? p0 : p0 + (r0 + 32 * wave) / a.group;                       // places of the wave's rows
     const int wmax = min(p0 + (r0 + 32 * wave + 31) / a.group, sp.pmax);
     const bool active = r0 + 32 * wave < rows;
     u4 bq[S];
@@ -100,6 +100,13 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
         qr.load(a.q, a.dtype, base + 8 * h, 16);
         f = a.scale * qr.convert(a.dtype, ok, max_halves, bq);
         if (a.cap_out == 0.0f) f *= kLog2e;
+    }
+    const int tok0 = r0 / a.group;
+    const KvTree tree(lds + 2 * kStage, a.max_new);
+    if constexpr (TREE) {
+        KvTree(tree).build(a.parents, s.first_row, min(s.m, a.max_new), tok0,
+                           (min(r0 + 32 * NW, rows) - 1) / a.group + 1 - tok0, a.window);
+        if (ok) place = p0 + tree.depth(tok - tok0);     // its position
     }
 
     // ---- tiles: codes to registers two tiles ahead, unpacked into LDS one ahead ----
@@ -227,15 +234,19 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
             }
             fl = 1.0f;
         }
-        if (t0 + 32 * TB - 1 > wmin || t0 <= kv_left_behind(a, wmax) || gone_blocks) {
+        if (t0 + 32 * TB - (TREE ? 0 : 1) > wmin || t0 <= kv_left_behind(a, wmax) || gone_blocks) {
             const int gone = kv_left_behind(a, place);
 #pragma unroll
             for (int u = 0; u < TB; ++u) {
                 const bool bad = (gone_blocks >> u) & 1;
+                uint32_t seen = 0u;                  // bit j: the row sees place t0 + 32 u + 4 h + j
+                // a block past the wave's last row is not in the tree's words
+                if constexpr (TREE) seen = t0 + 32 * u <= wmax ? tree.block(ok ? tok - tok0 : 0, t0 + 32 * u, p0) >> (4 * h) : 0u;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int tk = t0 + 32 * u + 8 * (e >> 2) + 4 * h + (e & 3);
-                    sc[u][e] = tk <= place && tk > gone && !bad ? sc[u][e] : -INFINITY;
+                    const bool near = TREE ? (seen >> (8 * (e >> 2) + (e & 3))) & 1u : tk <= place;
+                    sc[u][e] = near && tk > gone && !bad ? sc[u][e] : -INFINITY;
                 }
             }
         }
@@ -353,7 +364,11 @@ template <int D, int NW, bool PREC>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
     constexpr int lds = prompt_lds(D, PREC);
     const int64_t blocks = (int64_t)a.splits * a.c.heads * a.sq.batch * a.row_tiles;
-    hipLaunchKernelGGL((kv_prompt_kernel<D, NW, PREC>), dim3((unsigned)blocks), dim3(64 * NW), lds, s, a);
+    if (a.parents)
+        hipLaunchKernelGGL((kv_prompt_kernel<D, NW, PREC, true>), dim3((unsigned)blocks), dim3(64 * NW),
+                           lds + tree_lds(a, 32 * NW), s, a);
+    else
+        hipLaunchKernelGGL((kv_prompt_kernel<D, NW, PREC, false>), dim3((unsigned)blocks), dim3(64 * NW), lds, s, a);
     return hipGetLastError();
 }
 

@@ -53,7 +53,7 @@ __device__ __forceinline__ u2 word_pair(const uint8_t* plane, int g, int lane) {
     return *reinterpret_cast<const u2*>(plane + kv_word_off<G>(2 * g, lane));
 }
 
-template <int D>
+template <int D, bool TREE>
 __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnArgs a) {
     constexpr int G = D / 32, C = D / 16, kUnit = 36 * D, kLoads = (kUnit + 1023) / 1024;
     extern __shared__ __attribute__((aligned(16))) float smem[];
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
     const int r0 = rt0 * 16;
     if (r0 >= rows) return;
     const int nr = min(16, rows - r0);
-    const KvSpan sp = kv_span(a, s, r0, nr, split);
+    const KvSpan sp = kv_span<TREE>(a, s, r0, nr, split);
     auto out_row = [&](int row) -> int64_t {
         const int r = r0 + row, tok = r / a.group;
         return (s.first_row + tok) * a.hq + head * a.group + (r - tok * a.group);
@@ -103,7 +103,7 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
     u4 bq[G];
     const bool ok = i < nr;
     const int tok = ok ? (r0 + i) / a.group : 0, gh = ok ? r0 + i - tok * a.group : 0;
-    const int place = ok ? s.len - s.m + tok : sp.pmax;
+    int place = ok ? s.len - s.m + tok : sp.pmax;
     QueryRow<G> qr;
     qr.load(a.q, a.dtype, (s.first_row + tok) * a.q_ld + (int64_t)(head * a.group + gh) * D + 8 * qd, 32);
 
@@ -129,6 +129,12 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
         return ok;
     };
     bool have = n > 0 && fetch(0);
+    const int tok0 = r0 / a.group, p0 = s.len - s.m;
+    const KvTree tree(reinterpret_cast<uint8_t*>(smem) + a.tree_at, a.max_new);
+    if constexpr (TREE) {
+        KvTree(tree).build(a.parents, s.first_row, min(s.m, a.max_new), tok0, (r0 + nr - 1) / a.group + 1 - tok0, a.window);
+        if (ok) place = p0 + tree.depth(tok - tok0);          // its position
+    }
 
     float f = a.scale * qr.convert(a.dtype, ok, wave_max_rows, bq);
     if (a.cap_out == 0.0f) f *= kLog2e;
@@ -165,7 +171,7 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
         }
         const int t0 = (int)(32 * blk);
         const int tl = t0 + 16 * (qd >> 1) + 4 * (qd & 1);     // + 8 ab + j
-        const bool edge = t0 + 31 > sp.pmin || t0 <= kv_left_behind(a, sp.pmax);
+        const bool edge = t0 + (TREE ? 32 : 31) > sp.pmin || t0 <= kv_left_behind(a, sp.pmax);
         const bool tail = t0 + 32 > s.len;
         if (tail) {
             // places past the length may hold anything: their values' scales become 0 in the stage
@@ -209,10 +215,12 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
         }
         if (edge) {
             const int gone = kv_left_behind(a, place);
+            uint32_t seen = 0u;                              // bit j: the row sees place tl + j
+            if constexpr (TREE) seen = tree.block(ok ? tok - tok0 : 0, t0, p0) >> (tl - t0);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int t = tl + 8 * (e >> 2) + (e & 3);
-                x[e] = t <= place && t > gone ? x[e] : -INFINITY;
+                x[e] = (TREE ? (seen >> (t - tl)) & 1u : t <= place) && t > gone ? x[e] : -INFINITY;
             }
         }
         const float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * fl;
@@ -366,12 +374,17 @@ __global__ __launch_bounds__(THREADS) void kv_join_kernel(KvAttnArgs a) {
 }  // namespace
 
 template <int D>
-static hipError_t rows_launch(const KvAttnArgs& a, int waves, hipStream_t s) {
+static hipError_t rows_launch(KvAttnArgs a, int waves, hipStream_t s) {
     const int64_t blocks = (int64_t)a.splits * a.c.heads * a.sq.batch * a.row_tiles;
     const int rows = a.max_new * a.group < 16 ? a.max_new * a.group : 16;
     const size_t join = sizeof(float) * (size_t)waves * (32 + (size_t)rows * (D + 4)), ring = (size_t)waves * 2 * 36 * D;
     const size_t lds = join > ring ? join : ring;
-    hipLaunchKernelGGL((kv_rows_kernel<D>), dim3((unsigned)blocks), dim3(64 * waves), lds, s, a);
+    if (a.parents) {
+        a.tree_at = (int)lds;
+        hipLaunchKernelGGL((kv_rows_kernel<D, true>), dim3((unsigned)blocks), dim3(64 * waves), lds + tree_lds(a, 16), s, a);
+    } else {
+        hipLaunchKernelGGL((kv_rows_kernel<D, false>), dim3((unsigned)blocks), dim3(64 * waves), lds, s, a);
+    }
     return hipGetLastError();
 }
 

@@ -84,13 +84,14 @@ struct AttnSize {
     int group, max_new, max_ctx, window;
     float mean;                  // blocks of 32 keys that a row sees
     bool prec;                   // kv_prompt keeps the remainders of keys and values
+    bool tree;                   // any node of a tree may be a root: its window begins at the first one's
 
     // Blocks that some tile of `tile` rows may see: behind a window those of the window and of the
     // tile's own tokens, and its first row's window may begin and its last row's end inside a block.
     int64_t blocks(int tile) const {
         int64_t span = max_ctx;
         if (window) {
-            const int64_t own = (tile - 2) / group + 2, seen = window + (own < max_new ? own : max_new) + 30;
+            const int64_t own = tree ? max_new : (tile - 2) / group + 2, seen = window + (own < max_new ? own : max_new) + 30;
             span = seen < span ? seen : span;
         }
         return (span + kKvTok - 1) / kKvTok;
@@ -187,10 +188,10 @@ AttnPlan plan_prompt(const AttnSize& n) {
     return best;
 }
 
-AttnSize attention_size(int heads, int dim, int batch, int hq, int max_new, int max_ctx, int window, int dtype) {
+AttnSize attention_size(int heads, int dim, int batch, int hq, int max_new, int max_ctx, int window, int dtype, bool tree = false) {
     float mean = max_ctx > max_new ? max_ctx - 0.5f * max_new : 0.5f * max_ctx;
     if (window && window + 32.0f < mean) mean = window + 32.0f;
-    return AttnSize{heads, dim, batch, max_new * (hq / heads), hq / heads, max_new, max_ctx, window, mean / kKvTok, dtype != kBF16};
+    return AttnSize{heads, dim, batch, max_new * (hq / heads), hq / heads, max_new, max_ctx, window, mean / kKvTok, dtype != kBF16, tree};
 }
 
 // Many rows share a tile's unpacking but take 64 keys in turn after turn, few rows spread over the GPU;
@@ -228,6 +229,65 @@ q4gsw_status read_kernel(const q4gsw_kv_options* o, const q4gsw_kv_cache* c, int
     if (*kernel < Q4GSW_KV_ANY || *kernel > Q4GSW_KV_MANY_ROWS) return Q4GSW_E_ROUTE;
     if (*kernel == Q4GSW_KV_MANY_ROWS && (int64_t)max_new * (hq / c->heads) <= kFewRows) return Q4GSW_E_ROUTE;
     return Q4GSW_OK;
+}
+
+// kv_attention, or with `parents` attention of trees.
+q4gsw_status attend(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s, const int32_t* parents, bool tree, const void* q,
+                    int64_t q_ld, int32_t dtype, int32_t hq, int32_t max_new, int32_t max_ctx, int32_t window, float softcap,
+                    void* out, void* ws, uint64_t ws_bytes, const q4gsw_kv_options* opts, void* stream) {
+    KvAttnArgs a{};
+    Range cr;
+    q4gsw_status st = check_cache(c, &a.c, &cr);
+    if (st != Q4GSW_OK) return st;
+    if ((st = check_seqs(s, &a.sq)) != Q4GSW_OK) return st;
+    if ((st = check_attention(c, s->batch, s->tokens, hq, max_new, max_ctx)) != Q4GSW_OK) return st;
+    if (tree && max_new > kTreeMax) return Q4GSW_E_SHAPE;
+    if (window < 0 || !(softcap == 0.0f || (softcap >= kMinCap && softcap <= kMaxCap))) return Q4GSW_E_SHAPE;
+    if (!act_dtype_ok(dtype)) return Q4GSW_E_DTYPE;
+    int kernel = 0;
+    if ((st = read_kernel(opts, c, hq, max_new, &kernel)) != Q4GSW_OK) return st;
+    if (s->tokens == 0) return Q4GSW_OK;
+    if (!q || !out || (tree && !parents)) return Q4GSW_E_NULL;
+    const int64_t row = (int64_t)hq * c->dim;
+    const int es = esize(dtype);
+    if (q_ld < row || q_ld > kMaxDim) return Q4GSW_E_SHAPE;
+    if (!aligned16(q) || !aligned16(out) || (q_ld * es) % 16 != 0) return Q4GSW_E_ALIGN;
+    const AttnPlan p = plan_attention(attention_size(c->heads, c->dim, s->batch, hq, max_new, max_ctx, window, dtype, tree),
+                                      kernel);
+    const uint64_t need = plan_workspace(p, s->tokens, hq, c->dim);
+    // a grid takes fewer than 2^32 threads in one dimension; the join has up to 256 a row
+    if ((int64_t)p.splits * p.row_tiles > kMaxThreads / (64 * p.waves * ((int64_t)s->batch * c->heads)) ||
+        (p.splits > 1 && s->tokens * hq > kMaxThreads / 256))
+        return Q4GSW_E_SHAPE;
+    if (!ws_ok(ws, ws_bytes, need)) return Q4GSW_E_WORKSPACE;
+    const Range qr = range_of(q, rows_extent(s->tokens, q_ld, row, es));
+    const Range orr = range_of(out, (uint64_t)s->tokens * row * es), sr = range_of(ws, need);
+    if (overlap(orr, qr) || overlap(orr, cr) || overlap(sr, orr) || overlap(sr, qr) || overlap(sr, cr) ||
+        over_seqs(a.sq, orr) || over_seqs(a.sq, sr))
+        return Q4GSW_E_ALIAS;
+    const Range tr = range_of(parents, tree ? (uint64_t)s->tokens * 4 : 0);
+    if (overlap(orr, tr) || overlap(sr, tr)) return Q4GSW_E_ALIAS;
+    a.q = q;
+    a.q_ld = q_ld;
+    a.dtype = dtype;
+    a.out = out;
+    a.part = static_cast<float*>(ws);
+    a.ml = a.part + (uint64_t)p.splits * s->tokens * row;
+    a.hq = hq;
+    a.group = hq / c->heads;
+    a.max_new = max_new;
+    a.window = window;
+    a.cap_in = softcap > 0 ? 1.0f / softcap : 0.0f;
+    a.cap_out = softcap * kLog2e;
+    a.scale = 1.0f / __builtin_sqrtf((float)c->dim);
+    a.splits = p.splits;
+    a.chunk = p.chunk;
+    a.row_tiles = p.row_tiles;
+    a.parents = tree ? parents : nullptr;
+    hipStream_t st_ = static_cast<hipStream_t>(stream);
+    hipError_t e = p.prompt ? launch_kv_prompt(a, p.waves, st_) : launch_kv_rows(a, p.waves, st_);
+    if (e == hipSuccess && p.splits > 1) e = launch_kv_join(a, st_);
+    return hip_status(e);
 }
 
 }  // namespace
@@ -347,55 +407,58 @@ q4gsw_status q4gsw_kv_attention_ex(const q4gsw_kv_cache* c, const q4gsw_kv_seqs*
                                    int32_t dtype, int32_t hq, int32_t max_new, int32_t max_ctx, int32_t window,
                                    float softcap, void* out, void* ws, uint64_t ws_bytes, const q4gsw_kv_options* opts,
                                    void* stream) {
-    KvAttnArgs a{};
-    Range cr;
-    q4gsw_status st = check_cache(c, &a.c, &cr);
+    return attend(c, s, nullptr, false, q, q_ld, dtype, hq, max_new, max_ctx, window, softcap, out, ws, ws_bytes, opts, stream);
+}
+
+q4gsw_status q4gsw_kv_tree_attention_workspace_bytes(const q4gsw_kv_cache* c, int32_t batch, int64_t tokens, int32_t hq,
+                                                     int32_t max_new, int32_t max_ctx, uint64_t* bytes) {
+    if (max_new > kTreeMax) return bytes ? Q4GSW_E_SHAPE : Q4GSW_E_NULL;
+    return q4gsw_kv_attention_workspace_bytes(c, batch, tokens, hq, max_new, max_ctx, bytes);
+}
+
+q4gsw_status q4gsw_kv_tree_attention(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s, const int32_t* parents, const void* q,
+                                     int64_t q_ld, int32_t dtype, int32_t hq, int32_t max_new, int32_t max_ctx, int32_t window,
+                                     float softcap, void* out, void* ws, uint64_t ws_bytes, void* stream) {
+    return attend(c, s, parents, true, q, q_ld, dtype, hq, max_new, max_ctx, window, softcap, out, ws, ws_bytes, nullptr, stream);
+}
+
+q4gsw_status q4gsw_kv_tree_attention_ex(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s, const int32_t* parents,
+                                        const void* q, int64_t q_ld, int32_t dtype, int32_t hq, int32_t max_new,
+                                        int32_t max_ctx, int32_t window, float softcap, void* out, void* ws,
+                                        uint64_t ws_bytes, const q4gsw_kv_options* opts, void* stream) {
+    return attend(c, s, parents, true, q, q_ld, dtype, hq, max_new, max_ctx, window, softcap, out, ws, ws_bytes, opts, stream);
+}
+
+q4gsw_status q4gsw_kv_keep(const q4gsw_kv_cache* caches, int32_t count, const q4gsw_kv_seqs* s, const int32_t* parents,
+                           const int32_t* leaf, int32_t max_new, int32_t* kept, int32_t* path, void* stream) {
+    if (!caches) return Q4GSW_E_NULL;
+    if (count < 1 || count > kKeepCaches) return Q4GSW_E_SHAPE;
+    KvSeqs sv;
+    KvView cv[kKeepCaches];
+    Range cr[kKeepCaches];
+    for (int i = 0; i < count; ++i) {
+        const q4gsw_status st = check_cache(caches + i, cv + i, cr + i);
+        if (st != Q4GSW_OK) return st;
+        if (cv[i].pages != cv[0].pages || cv[i].page_size != cv[0].page_size || cv[i].heads != cv[0].heads ||
+            cv[i].dim != cv[0].dim)
+            return Q4GSW_E_SHAPE;
+    }
+    const q4gsw_status st = check_seqs(s, &sv);
     if (st != Q4GSW_OK) return st;
-    if ((st = check_seqs(s, &a.sq)) != Q4GSW_OK) return st;
-    if ((st = check_attention(c, s->batch, s->tokens, hq, max_new, max_ctx)) != Q4GSW_OK) return st;
-    if (window < 0 || !(softcap == 0.0f || (softcap >= kMinCap && softcap <= kMaxCap))) return Q4GSW_E_SHAPE;
-    if (!act_dtype_ok(dtype)) return Q4GSW_E_DTYPE;
-    int kernel = 0;
-    if ((st = read_kernel(opts, c, hq, max_new, &kernel)) != Q4GSW_OK) return st;
-    if (s->tokens == 0) return Q4GSW_OK;
-    if (!q || !out) return Q4GSW_E_NULL;
-    const int64_t row = (int64_t)hq * c->dim;
-    const int es = esize(dtype);
-    if (q_ld < row || q_ld > kMaxDim) return Q4GSW_E_SHAPE;
-    if (!aligned16(q) || !aligned16(out) || (q_ld * es) % 16 != 0) return Q4GSW_E_ALIGN;
-    const AttnPlan p = plan_attention(attention_size(c->heads, c->dim, s->batch, hq, max_new, max_ctx, window, dtype),
-                                      kernel);
-    const uint64_t need = plan_workspace(p, s->tokens, hq, c->dim);
-    // a grid takes fewer than 2^32 threads in one dimension; the join has up to 256 a row
-    if ((int64_t)p.splits * p.row_tiles > kMaxThreads / (64 * p.waves * ((int64_t)s->batch * c->heads)) ||
-        (p.splits > 1 && s->tokens * hq > kMaxThreads / 256))
-        return Q4GSW_E_SHAPE;
-    if (!ws_ok(ws, ws_bytes, need)) return Q4GSW_E_WORKSPACE;
-    const Range qr = range_of(q, rows_extent(s->tokens, q_ld, row, es));
-    const Range orr = range_of(out, (uint64_t)s->tokens * row * es), sr = range_of(ws, need);
-    if (overlap(orr, qr) || overlap(orr, cr) || overlap(sr, orr) || overlap(sr, qr) || overlap(sr, cr) ||
-        over_seqs(a.sq, orr) || over_seqs(a.sq, sr))
-        return Q4GSW_E_ALIAS;
-    a.q = q;
-    a.q_ld = q_ld;
-    a.dtype = dtype;
-    a.out = out;
-    a.part = static_cast<float*>(ws);
-    a.ml = a.part + (uint64_t)p.splits * s->tokens * row;
-    a.hq = hq;
-    a.group = hq / c->heads;
-    a.max_new = max_new;
-    a.window = window;
-    a.cap_in = softcap > 0 ? 1.0f / softcap : 0.0f;
-    a.cap_out = softcap * kLog2e;
-    a.scale = 1.0f / __builtin_sqrtf((float)c->dim);
-    a.splits = p.splits;
-    a.chunk = p.chunk;
-    a.row_tiles = p.row_tiles;
-    hipStream_t st_ = static_cast<hipStream_t>(stream);
-    hipError_t e = p.prompt ? launch_kv_prompt(a, p.waves, st_) : launch_kv_rows(a, p.waves, st_);
-    if (e == hipSuccess && p.splits > 1) e = launch_kv_join(a, st_);
-    return hip_status(e);
+    if (max_new < 1 || max_new > kTreeMax || (int64_t)sv.batch * cv[0].heads > kMaxThreads / 256) return Q4GSW_E_SHAPE;
+    if (!leaf || !kept || (sv.tokens > 0 && !parents)) return Q4GSW_E_NULL;
+    const Range kr = range_of(kept, (uint64_t)sv.batch * 4), pr = range_of(path, path ? (uint64_t)sv.batch * max_new * 4 : 0);
+    const Range ins[2] = {range_of(parents, (uint64_t)sv.tokens * 4), range_of(leaf, (uint64_t)sv.batch * 4)};
+    if (overlap(kr, pr) || over_seqs(sv, kr) || over_seqs(sv, pr)) return Q4GSW_E_ALIAS;
+    for (const Range& in : ins)
+        if (overlap(in, kr) || overlap(in, pr)) return Q4GSW_E_ALIAS;
+    for (int i = 0; i < count; ++i) {
+        if (over_seqs(sv, cr[i]) || overlap(cr[i], kr) || overlap(cr[i], pr) || overlap(cr[i], ins[0]) || overlap(cr[i], ins[1]))
+            return Q4GSW_E_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(cr[i], cr[j])) return Q4GSW_E_ALIAS;
+    }
+    return hip_status(launch_kv_keep(cv, count, sv, parents, leaf, max_new, kept, path, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

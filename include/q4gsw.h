@@ -514,6 +514,48 @@ q4gsw_status q4gsw_kv_attention_plan(const q4gsw_kv_cache *c, int32_t batch, int
                                      int32_t max_new, int32_t max_ctx, int32_t window, int32_t dtype,
                                      const q4gsw_kv_options *opts, q4gsw_kv_plan_info *info);
 
+/*
+ * Trees of drafted tokens over the cache.  The m new tokens of a sequence, its token rows in their order, are
+ * nodes 0 .. m - 1 of a tree: parents[r] (device int32 [tokens]) of the row of node i is its parent's
+ * number, below i; any other value makes the node a root.  The nodes' keys and values are in the cache
+ * at the places of new tokens, p0 .. p0 + m - 1 behind the p0 = lens[b] - m tokens before the tree
+ * (q4gsw_kv_append stores them).
+ *
+ * q4gsw_kv_tree_attention: q4gsw_kv_attention in which a node sees the tokens before the tree, its ancestors
+ * and itself, and with window > 0 those of them whose position is above its own - window.  A node's
+ * position is p0 + its depth (a root's is 0).  Everything else as q4gsw_kv_attention, its errors too;
+ *   max_new at most 512 (E_SHAPE); nodes past max_new are left undefined and no node has them as ancestors
+ * E_NULL (parents), E_ALIAS (out or ws overlaps parents).
+ */
+q4gsw_status q4gsw_kv_tree_attention_workspace_bytes(const q4gsw_kv_cache *c, int32_t batch, int64_t tokens,
+                                                     int32_t hq, int32_t max_new, int32_t max_ctx, uint64_t *bytes);
+q4gsw_status q4gsw_kv_tree_attention(const q4gsw_kv_cache *c, const q4gsw_kv_seqs *s, const int32_t *parents,
+                                     const void *q, int64_t q_ld, int32_t dtype, int32_t hq, int32_t max_new,
+                                     int32_t max_ctx, int32_t window, float softcap, void *out, void *ws,
+                                     uint64_t ws_bytes, void *stream);
+/* With a per-call choice of the kernel (opts NULL: the same call). */
+q4gsw_status q4gsw_kv_tree_attention_ex(const q4gsw_kv_cache *c, const q4gsw_kv_seqs *s, const int32_t *parents,
+                                        const void *q, int64_t q_ld, int32_t dtype, int32_t hq, int32_t max_new,
+                                        int32_t max_ctx, int32_t window, float softcap, void *out, void *ws,
+                                        uint64_t ws_bytes, const q4gsw_kv_options *opts, void *stream);
+/*
+ * The accepted path of each tree in a row: nodes n_0 < n_1 < .. on the way from a root to node leaf[b]
+ * (device int32 [batch]; a number outside the sequence's nodes or past max_new: no node) move to places
+ * p0, p0 + 1, .., as they are, in each of `count` (1..128) caches of one shape that share the sequences'
+ * tables (a model's layers).  Places behind the path keep what they hold.
+ *   kept  device int32 [batch] (written): tokens of the sequence then, p0 + the path's length (at least 0):
+ *         the lens of what comes next, less its new tokens
+ *   path  device int32 [batch][max_new] (written), or NULL: n_0, n_1, .., then -1
+ *   max_new  1..512: later nodes are not looked at
+ * A node whose place is on no page counts as zeros.  Pages written by one call must not be shared by its
+ * sequences.
+ * E_NULL, E_SHAPE (count, max_new, caches of unlike shapes), E_BUFFER, E_ALIGN, E_ALIAS (an output
+ * overlaps another, an input or a cache; caches overlap each other or an input), E_HIP.
+ */
+q4gsw_status q4gsw_kv_keep(const q4gsw_kv_cache *caches, int32_t count, const q4gsw_kv_seqs *s,
+                           const int32_t *parents, const int32_t *leaf, int32_t max_new, int32_t *kept,
+                           int32_t *path, void *stream);
+
 /* Route attestation: the q4gsw_route_id a plain call (no options) with these
  * arguments takes (Q4GSW_ROUTE_NONE if it would fail validation).  For
  * Q4GSW_OP_QKV pass Wq.  This is the attestation of the WebGPU SDPA routing pull
