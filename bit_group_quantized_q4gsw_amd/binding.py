@@ -77,6 +77,24 @@ class KvSeqs(ctypes.Structure):
                 ("tokens", ctypes.c_int64)]
 
 
+class AdaptersDesc(ctypes.Structure):
+    """q4gsw_adapters of include/q4gsw.h."""
+    _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("slots", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("data", ctypes.c_void_p),
+                ("bytes", ctypes.c_uint64)]
+
+
+class LogitsRules(ctypes.Structure):
+    """q4gsw_logits_rules of include/q4gsw.h."""
+    _fields_ = [("batch", ctypes.c_int32), ("max_new", ctypes.c_int32), ("cu", ctypes.c_void_p),
+                ("history", ctypes.c_void_p), ("history_ld", ctypes.c_int64), ("history_cols", ctypes.c_int32),
+                ("bias_cols", ctypes.c_int32), ("history_len", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p),
+                ("ids", ctypes.c_void_p), ("parents", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("bias_ld", ctypes.c_int64), ("mask", ctypes.c_void_p),
+                ("mask_ld", ctypes.c_int64)]
+
+
 class KvPlanInfo(ctypes.Structure):
     """q4gsw_kv_plan_info of include/q4gsw.h."""
     _fields_ = [("kernel", ctypes.c_int32), ("waves", ctypes.c_int32), ("splits", ctypes.c_int32)]
@@ -123,6 +141,7 @@ def lib() -> ctypes.CDLL:
         pw = ctypes.POINTER(WeightDesc)
         po = ctypes.POINTER(Options)
         ko = ctypes.POINTER(KvOptions)
+        pa = ctypes.POINTER(AdaptersDesc)
         pc, ps = ctypes.POINTER(KvCacheDesc), vp       # sequences: a KvSeqs by reference or its packed bytes
         sigs = {
             "q4gsw_packed_bytes": [i64, i64, i64, i32, ctypes.POINTER(u64)],
@@ -165,6 +184,12 @@ def lib() -> ctypes.CDLL:
             "q4gsw_adapter_workspace_bytes": [i32, pw, i64, i32, i32, ctypes.POINTER(u64)],
             "q4gsw_adapter_fwd": [pw, vp, i32, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, u64, vp],
             "q4gsw_adapter_bwd": [pw, vp, vp, i32, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, vp, vp, u64, vp],
+            "q4gsw_logits_adjust": [vp, i32, i64, i64, i64, vp, vp, i64, vp],
+            "q4gsw_adapters_bytes": [pa, ctypes.POINTER(u64)],
+            "q4gsw_adapters_load": [pa, i32, vp, vp, i32, i32, ctypes.c_float, vp],
+            "q4gsw_adapters_workspace_bytes": [pa, pw, i64, i32, ctypes.POINTER(u64)],
+            "q4gsw_adapters_add": [pa, vp, i32, i64, vp, vp, vp, vp, u64, vp],
+            "q4gsw_adapters_fwd": [pw, pa, vp, i32, i64, vp, vp, vp, u64, vp],
             "q4gsw_adamw_step": [vp, vp, vp, vp, i64, ctypes.POINTER(AdamwParams), i64, vp],
         }
         for name, args in sigs.items():
@@ -699,6 +724,108 @@ def kv_keep(caches, parents: torch.Tensor, leaf: torch.Tensor, table: torch.Tens
     return kept, path
 
 
+# q4gsw_logits_rules as packed bytes, as with the sequences.
+_pack_rules = struct.Struct("iiPPqiiPPPPPPPPPqPq").pack
+
+
+def _table(t: torch.Tensor, dtype: torch.dtype, rows: int, dev: int, name: str) -> Tuple[int, int, int]:
+    """(address, row pitch, columns) of a [rows, columns] tensor of dense rows."""
+    if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != rows or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor [{rows}, columns] on cuda:{dev}")
+    cols = t.shape[1]
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must have dense rows")
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return t.data_ptr(), ld, cols
+
+
+def logits_adjust(logits: torch.Tensor, cu: Optional[torch.Tensor] = None, max_new: int = 1,
+                  history: Optional[torch.Tensor] = None, history_lens: Optional[torch.Tensor] = None,
+                  prompt_lens: Optional[torch.Tensor] = None, ids: Optional[torch.Tensor] = None,
+                  parents: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
+                  presence: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,
+                  bias_ids: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  mask: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out [rows, V] of logits' dtype (may be logits itself): x of a token seen so far divided by repetition
+    where it is positive, else multiplied; of one generated n times lowered by frequency n + presence; bias
+    added; -inf where the mask does not allow it.
+
+    Row r is sequence r's, or with cu (int32 [batch + 1]) rows cu[b] .. cu[b + 1] - 1 are sequence b's, of which
+    those past max_new and those of no sequence are left as they are.  Per sequence: history (int32 [batch,
+    columns]; the first history_lens[b] tokens, prompt_lens[b] of them only seen), repetition, presence and
+    frequency (fp32 [batch]), bias_ids (int32 [batch, columns]) with bias (fp32): of entries with one token the
+    last counts.  Per row: ids (int32 [rows]), the rows' own tokens, which count as generated with those of the
+    rows before them in the sequence, or with parents (as in kv_tree_attention) with those of their
+    ancestors; mask (int32 [rows, ceil(V / 32)]), bit v % 32 of word v // 32 allows token v."""
+    code = _TORCH_DTYPE.get(logits.dtype)
+    dev = logits.get_device()
+    if logits.dim() != 2 or code is None or dev < 0:
+        raise ValueError("logits must be a floating GPU tensor [rows, V]")
+    rows, V = logits.shape
+    if out is None:
+        out = torch.empty(rows, V, dtype=logits.dtype, device=logits.device)
+    elif out.dtype is not logits.dtype or out.shape != logits.shape or out.get_device() != dev:
+        raise ValueError(f"out must be a {logits.dtype} tensor [{rows}, {V}] on cuda:{dev}")
+    pitches = []
+    for t, name in ((logits, "logits"), (out, "out")):
+        ld, step = t.stride()
+        if rows <= 1:
+            ld = V
+        if (V > 1 and step != 1) or ld < V:
+            raise ValueError(f"{name} must have dense rows")
+        pitches.append(ld)
+    batch, cp = rows, None
+    if cu is not None:
+        if cu.dim() != 1 or cu.numel() < 2:
+            raise ValueError("cu must be an int32 tensor [batch + 1]")
+        batch = cu.numel() - 1
+        cu = _per_row(cu, batch + 1, dev, "cu")
+        cp = cu.data_ptr()
+    _int32(max_new)
+    keep = [cu]                                       # dense copies live until the launch
+    def one(t, n, name, dtype=torch.int32):
+        if t is None:
+            return None
+        if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or t.get_device() != dev:
+            raise ValueError(f"{name} must be a {dtype} tensor [{n}] on cuda:{dev}")
+        if not t.is_contiguous():
+            t = t.contiguous()
+            keep.append(t)
+        return t.data_ptr()
+    hp = bp = vp = mp = None
+    h_ld = h_cols = b_ld = b_cols = m_ld = 0
+    if history is not None:
+        hp, h_ld, h_cols = _table(history, torch.int32, batch, dev, "history")
+        if history_lens is None:
+            raise ValueError("history needs history_lens")
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    if bias is not None:
+        bp, b_ld, b_cols = _table(bias_ids, torch.int32, batch, dev, "bias_ids")
+        vp, v_ld, v_cols = _table(bias, torch.float32, batch, dev, "bias")
+        if v_cols != b_cols or v_ld != b_ld:
+            raise ValueError("bias must have bias_ids' shape and strides")
+    if mask is not None:
+        mp, m_ld, m_cols = _table(mask, torch.int32, rows, dev, "mask")
+        if m_cols < (V + 31) // 32:
+            raise ValueError("mask must have a bit for every token")
+    if parents is not None and (ids is None or cu is None):
+        raise ValueError("parents need ids and cu")
+    f32 = torch.float32
+    rules = _pack_rules(batch, max_new, cp or 0, hp or 0, h_ld, h_cols, b_cols, one(history_lens, batch, "history_lens") or 0,
+                        one(prompt_lens, batch, "prompt_lens") or 0, one(ids, rows, "ids") or 0,
+                        one(parents, rows, "parents") or 0, one(repetition, batch, "repetition", f32) or 0,
+                        one(presence, batch, "presence", f32) or 0, one(frequency, batch, "frequency", f32) or 0, bp or 0,
+                        vp or 0, b_ld, mp or 0, m_ld)
+    _check(lib().q4gsw_logits_adjust(logits.data_ptr(), code, rows, V, pitches[0], rules, out.data_ptr(), pitches[1],
+                                     _stream_of(dev)), "q4gsw_logits_adjust")
+    return out
+
+
 def adapter_workspace_bytes(op: int, w: PackedWeight, M: int, dtype: torch.dtype, rank: int) -> int:
     out = ctypes.c_uint64()
     _check(lib().q4gsw_adapter_workspace_bytes(op, w.ref(), M, _TORCH_DTYPE[dtype], rank, ctypes.byref(out)),
@@ -755,6 +882,93 @@ def adapter_bwd(w: PackedWeight, x: torch.Tensor, d_out: torch.Tensor, A: torch.
                                    B.data_ptr(), r, float(alpha), t.data_ptr(), dx.data_ptr(), dA.data_ptr(),
                                    dB.data_ptr(), wp, wb, _stream()), "q4gsw_adapter_bwd")
     return dx, dA, dB
+
+
+class Adapters:
+    """Low-rank adapters in the slots of one set: the descriptor and its device buffer."""
+
+    def __init__(self, desc: AdaptersDesc, buffer: torch.Tensor):
+        self.desc = desc
+        self.buffer = buffer
+        self.slots, self.rank, self.N, self.K = desc.slots, desc.rank, desc.N, desc.K
+        self._ref = ctypes.byref(desc)
+        self._dev = buffer.get_device()
+
+
+def adapters(slots: int, rank: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16, device="cuda") -> Adapters:
+    """An empty set (no slot adds anything) of `slots` adapters of up to `rank` beside a projection [N, K], its
+    factors held in `dtype` (bf16 or fp16)."""
+    _int32(slots, rank)
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("dtype must be torch.float16 or torch.bfloat16")
+    desc = AdaptersDesc(N, K, slots, rank, _TORCH_DTYPE[dtype], 0, None, 0)
+    out = ctypes.c_uint64()
+    _check(lib().q4gsw_adapters_bytes(ctypes.byref(desc), ctypes.byref(out)), "q4gsw_adapters_bytes")
+    buf = torch.zeros(out.value, dtype=torch.uint8, device=device)
+    if not buf.is_cuda:
+        raise ValueError("a set of adapters lives on a GPU")
+    desc.data, desc.bytes = buf.data_ptr(), out.value
+    return Adapters(desc, buf)
+
+
+def adapters_load(s: Adapters, slot: int, A: torch.Tensor, B: torch.Tensor, alpha: float) -> None:
+    """The adapter A [r, K], B [N, r] (r up to the set's rank; rounded once to its type), scaled by alpha, into a
+    slot."""
+    _int32(slot)
+    r = A.shape[0] if A.dim() == 2 else 0
+    code = _TORCH_DTYPE.get(A.dtype)
+    if tuple(A.shape) != (r, s.K) or tuple(B.shape) != (s.N, r) or code is None or B.dtype is not A.dtype \
+            or A.get_device() != s._dev or B.get_device() != s._dev:
+        raise ValueError(f"A must be [r, {s.K}] and B [{s.N}, r], of one floating type, on {s.buffer.device}")
+    A, B = A.contiguous(), B.contiguous()
+    _check(lib().q4gsw_adapters_load(s._ref, slot, A.data_ptr(), B.data_ptr(), code, r, float(alpha), _stream_of(s._dev)),
+           "q4gsw_adapters_load")
+
+
+def adapters_workspace_bytes(s: Adapters, M: int, dtype: torch.dtype, w: Optional[PackedWeight] = None) -> int:
+    """Workspace of adapters_fwd with the weight w, or of adapters_add, on M rows of `dtype`."""
+    out = ctypes.c_uint64()
+    _check(lib().q4gsw_adapters_workspace_bytes(s._ref, w.ref() if w is not None else None, M, _TORCH_DTYPE[dtype],
+                                                ctypes.byref(out)), "q4gsw_adapters_workspace_bytes")
+    return out.value
+
+
+def _adapter_rows(x: torch.Tensor, s: Adapters, slots: torch.Tensor) -> Tuple[torch.Tensor, int, torch.Tensor, int]:
+    code = _TORCH_DTYPE.get(x.dtype)
+    if x.dim() != 2 or x.shape[1] != s.K or code is None or x.get_device() != s._dev:
+        raise ValueError(f"x must be a floating tensor [M, {s.K}] on {s.buffer.device}")
+    M = x.shape[0]
+    return x.contiguous(), code, _per_row(slots, M, s._dev, "slots"), M
+
+
+def adapters_fwd(w: PackedWeight, x: torch.Tensor, s: Adapters, slots: torch.Tensor, out: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [M, N] fp32: y[m] = x[m] . dequant(W)^T + alpha_i (x[m] A_i^T) B_i^T for the adapter in slot i = slots[m]
+    (int32 [M]; outside the set's slots: none)."""
+    x, code, slots, M = _adapter_rows(x, s, slots)
+    y = _out(out, (M, s.N), x.device, "out")
+    need = adapters_workspace_bytes(s, M, x.dtype, w)
+    ws, wp, wb = _ws_args(need, workspace, x.device)
+    _check(lib().q4gsw_adapters_fwd(w.ref(), s._ref, x.data_ptr(), code, M, slots.data_ptr(), y.data_ptr(), wp, wb,
+                                    _stream_of(s._dev)), "q4gsw_adapters_fwd")
+    return y
+
+
+def adapters_add(y: torch.Tensor, x: torch.Tensor, s: Adapters, slots: torch.Tensor, out: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out [M, N] fp32: y[m] (fp32; a projection of the same rows) + alpha_i (x[m] A_i^T) B_i^T for the adapter in
+    slot i = slots[m].  `out` may be y itself."""
+    x, code, slots, M = _adapter_rows(x, s, slots)
+    if y.dtype is not torch.float32 or tuple(y.shape) != (M, s.N) or y.get_device() != s._dev:
+        raise ValueError(f"y must be an fp32 tensor [{M}, {s.N}] on {s.buffer.device}")
+    if out is not y:
+        y = y.contiguous()
+    out = _out(out, (M, s.N), x.device, "out")
+    need = adapters_workspace_bytes(s, M, x.dtype)
+    ws, wp, wb = _ws_args(need, workspace, x.device)
+    _check(lib().q4gsw_adapters_add(s._ref, x.data_ptr(), code, M, slots.data_ptr(), y.data_ptr(), out.data_ptr(), wp, wb,
+                                    _stream_of(s._dev)), "q4gsw_adapters_add")
+    return out
 
 
 def adamw_step(param: torch.Tensor, grad: torch.Tensor, exp_avg: torch.Tensor, exp_avg_sq: torch.Tensor,

@@ -1,0 +1,467 @@
+// Low-rank adapters of many requests beside one projection (gfx950).
+//
+//   out[m] = y[m] + alpha_s (x[m] A_s^T) B_s^T,   s = slot[m];  A_s [rank, K], B_s [N, rank].
+//
+// A set holds its slots' factors in 16 bits, laid out when a slot is loaded for the matrix operands that
+// read them (adapter_set.h), so odd ranks, widths and alignments cost nothing later.  Two launches:
+//   * t[m] = x[m] A_s^T, K cut into chunks: a wave takes 16 rows, one of the adapters among them, 16 ranks
+//     and one chunk; factors as the first operand of the 16x16x32 product, rows as the second.  Rows of
+//     other adapters are not loaded: they are zeros there, and their columns of the product are not stored;
+//   * out = y + alpha t B_s^T: a workgroup adds the chunks' t once (in a fixed order), and its waves walk the
+//     adapters of the 16 rows; factors as the first operand of the 16x16x16 product, so that a lane ends
+//     with eight neighbouring columns of one row.
+// Rows need no order: adapters are found among each 16 rows by comparison, and one that many tiles share
+// is read from L2 by all but the first.
+//
+// Numbers: products of 16-bit factors are exact in the matrix unit's fp32, so what rows and t lose on
+// their way into 16-bit operands is all that is lost.  They enter as sums of parts: with bf16 factors one
+// part of a bf16 row, two of fp16 (exact: 11 bits in 8 + 8), three of fp32 (exact: 24 in 3 x 8) and of t; with
+// fp16 factors, after a power of two per row (and, in x, per 256 columns) that brings the largest value to
+// 2^14, one part of an fp16 row (as it is) or bf16 row, two of fp32 and of t (22 bits of the largest).
+#include "adapter_set.h"
+#include "internal.h"
+#include "kv_attention.h"   // row_factor, wave_max_rows
+
+namespace q4gsw {
+namespace {
+
+constexpr int kSub = 256;            // columns of x loaded at a time: 8 steps of 32
+
+typedef short s4v __attribute__((ext_vector_type(4)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+
+template <int FT>
+__device__ __forceinline__ f4 mfma32(u4 a, u4 b, f4 c) {
+    if constexpr (FT == kF16) return mfma_f16(a, b, c);
+    else return mfma_bf16(a, b, c);
+}
+// 16x16x16: lane l holds A[l % 16][4 (l / 16) + 0..3], B[4 (l / 16) + 0..3][l % 16]; D as in 16x16x32.
+template <int FT>
+__device__ __forceinline__ f4 mfma16(u2 a, u2 b, f4 c) {
+    if constexpr (FT == kF16) return __builtin_amdgcn_mfma_f32_16x16x16f16(bitcast<h4>(a), bitcast<h4>(b), c, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(bitcast<s4v>(a), bitcast<s4v>(b), c, 0, 0, 0);
+}
+
+template <int FT, int XT>
+constexpr int row_parts() {
+    if (FT == XT) return 1;
+    if (FT == kF16) return XT == kF32 ? 2 : 1;
+    return XT == kF32 ? 3 : 2;
+}
+
+// v0 and v1 as one pair of a part, which is taken off them.
+template <int FT>
+__device__ __forceinline__ uint32_t take_part(float& v0, float& v1) {
+    if constexpr (FT == kF16) {
+        const h2 p = {(_Float16)v0, (_Float16)v1};
+        v0 -= (float)p[0];
+        v1 -= (float)p[1];
+        return bitcast<uint32_t>(p);
+    } else {
+        const uint32_t p = bitcast<uint32_t>(b2{(__bf16)v0, (__bf16)v1});
+        v0 -= bitcast<float>(p << 16);
+        v1 -= bitcast<float>(p & 0xFFFF0000u);
+        return p;
+    }
+}
+
+// The adapters among 16 rows: `mine` is the slot of row lane % 16 (-1: none); bit i of the result: row i
+// is the first of its adapter.
+__device__ __forceinline__ int row_slot(const AdapterArgs& a, int64_t tile, int i) {
+    const int64_t m = 16 * tile + i;
+    const int s = m < a.M ? a.slot[m] : -1;
+    return s >= 0 && s < a.set.slots ? s : -1;
+}
+__device__ __forceinline__ uint32_t first_rows(int mine, int i) {
+    bool again = mine < 0;
+#pragma unroll
+    for (int j = 0; j < 15; ++j) again |= j < i && __builtin_amdgcn_readlane(mine, j) == mine;
+    return (uint32_t)__ballot(!again) & 0xFFFFu;
+}
+
+// Columns k .. k + 7 of a row of x, as they lie in memory; zeros past K.
+template <int XT, bool VEC>
+struct Octet {
+    u4 w[XT == kF32 ? 2 : 1];
+    __device__ __forceinline__ void clear() {
+        for (u4& v : w) v = u4{0u, 0u, 0u, 0u};
+    }
+    __device__ __forceinline__ void load(const void* x, int64_t row, int64_t k, int64_t K) {
+        if constexpr (VEC && XT == kF32) {
+            if (k < K) w[0] = ldg16(static_cast<const float*>(x) + row + k);
+            if (k + 4 < K) w[1] = ldg16(static_cast<const float*>(x) + row + k + 4);
+        } else if constexpr (VEC) {
+            if (k < K) w[0] = ldg16(static_cast<const uint16_t*>(x) + row + k);
+        } else if constexpr (XT == kF32) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (k + e < K) w[e >> 2][e & 3] = static_cast<const uint32_t*>(x)[row + k + e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (k + e < K) w[0][e >> 1] |= (uint32_t)static_cast<const uint16_t*>(x)[row + k + e] << (16 * (e & 1));
+        }
+    }
+    __device__ __forceinline__ float operator[](int e) const {
+        if constexpr (XT == kF32) return bitcast<float>(w[e >> 2][e & 3]);
+        else if constexpr (XT == kF16) return (float)bitcast<h2>(w[0][e >> 1])[e & 1];
+        else return bitcast<float>((e & 1) ? w[0][e >> 1] & 0xFFFF0000u : w[0][e >> 1] << 16);
+    }
+};
+
+// t of 16 rows, 16 ranks and one chunk, a wave: part[chunk][m][rank].
+template <int FT, int XT, bool VEC>
+__global__ __launch_bounds__(256) void down_kernel(AdapterArgs a) {
+    constexpr int P = row_parts<FT, XT>();
+    constexpr bool SCALED = FT == kF16 && XT != kF16;
+    constexpr int kSteps = kSub / 32;
+    const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int64_t id = blockIdx.x;
+    const int chunk = (int)(id % a.chunk_groups) * 4 + wave;
+    id /= a.chunk_groups;
+    const int rt = (int)(id % a.rank_tiles);
+    id /= a.rank_tiles;
+    const int group = (int)(id % a.groups);
+    const int64_t tile = id / a.groups;
+    if (chunk >= a.chunks) return;
+    const int mine = row_slot(a, tile, i);
+    uint32_t firsts = first_rows(mine, i);
+    const int64_t m = 16 * tile + i, row = m * a.K;
+    const int64_t steps = a.set.k_pad >> 5;
+    for (int n = 0; firsts; firsts &= firsts - 1, ++n) {
+        if (n % a.groups != group) continue;
+        const int slot = __builtin_amdgcn_readlane(mine, __builtin_ctz(firsts));
+        const bool match = mine == slot;
+        const uint8_t* A = a.set.data + slot * a.set.slot_bytes + 1024 * (int64_t)rt + 16 * lane;
+        f4 sum = {0.f, 0.f, 0.f, 0.f};
+        for (int sub = 0; sub < a.subs; ++sub) {
+            const int64_t s0 = ((int64_t)chunk * a.subs + sub) * kSteps;
+            u4 av[kSteps];
+            Octet<XT, VEC> xv[kSteps];
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                av[s] = u4{0u, 0u, 0u, 0u};
+                xv[s].clear();
+                if (s0 + s < steps) av[s] = ldg16(A + (s0 + s) * a.rank_tiles * 1024);
+            }
+            if (match) {
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) xv[s].load(a.x, row, 32 * (s0 + s) + 8 * q, a.K);
+            }
+            float mul = 1.0f, inv = 1.0f;
+            if constexpr (SCALED) {
+                float amax = 0.0f;
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(xv[s][e]));
+                row_factor(wave_max_rows(amax), mul, inv);
+            }
+            f4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                if constexpr (FT == XT) {
+                    acc = mfma32<FT>(av[s], xv[s].w[0], acc);
+                } else {
+                    u4 part[P];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v0 = xv[s][2 * e], v1 = xv[s][2 * e + 1];
+                        if constexpr (SCALED) {
+                            v0 *= mul;
+                            v1 *= mul;
+                        }
+#pragma unroll
+                        for (int p = 0; p < P; ++p) part[p][e] = take_part<FT>(v0, v1);
+                    }
+#pragma unroll
+                    for (int p = 0; p < P; ++p) acc = mfma32<FT>(av[s], part[p], acc);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = SCALED ? fmaf(acc[e], inv, sum[e]) : sum[e] + acc[e];
+        }
+        // lane (i, q) holds ranks 4 q .. + 3 of row i
+        if (match) *reinterpret_cast<f4*>(a.part + (chunk * a.M + m) * (16 * a.rank_tiles) + 16 * rt + 4 * q) = sum;
+    }
+}
+
+// out = y + alpha t B^T for 16 rows and 128 J columns, S steps of 16 ranks.
+template <int FT, int S, int J>
+__global__ __launch_bounds__(256) void up_kernel(AdapterArgs a) {
+    constexpr int G = S == 1 ? 4 : (S == 2 ? 2 : 1);      // groups of threads that add t's chunks
+    constexpr int kBatch = J * S <= 4 ? 4 : 1;            // adapters whose factors are loaded together
+    constexpr int P = FT == kF16 ? 2 : 3;
+    __shared__ f4 s_t[G][64 * S];
+    const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t tile = blockIdx.x / a.col_groups, m = 16 * tile + i;
+    const int64_t blk0 = (int64_t)(blockIdx.x % a.col_groups) * 4 * J + wave * J;
+    const int mine = row_slot(a, tile, i);
+    uint32_t firsts = first_rows(mine, i);
+    if (!firsts && a.y == a.out) return;
+
+    // what the columns hold so far
+    f4 acc[J][2], base[J][2];
+    auto col = [&](int j, int h) -> int64_t { return 32 * (blk0 + j) + 8 * q + 4 * h; };
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            acc[j][h] = base[j][h] = f4{0.f, 0.f, 0.f, 0.f};
+            const int64_t n = col(j, h);
+            if (m < a.M) {
+                if (a.quads) {
+                    if (n < a.N) base[j][h] = *reinterpret_cast<const f4*>(a.y + m * a.N + n);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < a.N) base[j][h][e] = a.y[m * a.N + n + e];
+                }
+            }
+        }
+
+    // t of the 16 rows: thread (g, s, q, i) adds every G-th chunk of four ranks of a row
+    const int g = tid / (64 * S);
+    if (g < G) {
+        const int s = (tid / 64) % S;
+        f4 t = {0.f, 0.f, 0.f, 0.f};
+        if (mine >= 0) {
+            const int64_t at = m * (16 * S) + 16 * s + 4 * q;
+            constexpr int kLoads = 4;
+            for (int c0 = g; c0 < a.chunks; c0 += kLoads * G) {
+                f4 v[kLoads];
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) {
+                    const int c = c0 + k * G;
+                    v[k] = *reinterpret_cast<const f4*>(a.part + (c < a.chunks ? c : c0) * a.M * (16 * S) + at);
+                }
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) {
+                    if (c0 + k * G >= a.chunks) break;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) t[e] += v[k][e];
+                }
+            }
+        }
+        s_t[g][64 * s + lane] = t;
+    }
+    const float alpha = mine >= 0 ? a.set.alpha[mine] : 0.0f;
+    __syncthreads();
+    float tv[S][4];
+    float amax = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float v = s_t[0][64 * s + lane][e];
+#pragma unroll
+            for (int k = 1; k < G; ++k) v += s_t[k][64 * s + lane][e];
+            tv[s][e] = v * alpha;
+            amax = fmaxf(amax, fabsf(tv[s][e]));
+        }
+    float mul = 1.0f, inv = 1.0f;
+    if constexpr (FT == kF16) row_factor(wave_max_rows(amax), mul, inv);
+    u2 part[S][P];
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float v0 = tv[s][2 * e] * mul, v1 = tv[s][2 * e + 1] * mul;
+#pragma unroll
+            for (int p = 0; p < P; ++p) part[s][p][e] = take_part<FT>(v0, v1);
+        }
+
+    const int64_t blocks = a.set.n_pad >> 5;
+    while (firsts) {
+        int slot[kBatch];
+        u4 b[kBatch][J][S];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            slot[k] = -1;
+            if (!firsts) continue;
+            slot[k] = __builtin_amdgcn_readlane(mine, __builtin_ctz(firsts));
+            firsts &= firsts - 1;
+            const uint8_t* B = a.set.data + slot[k] * a.set.slot_bytes + a.set.b_offset + 16 * lane;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    if (blk0 + j < blocks) b[k][j][s] = ldg16(B + ((blk0 + j) * S + s) * 1024);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (slot[k] < 0) break;
+            // a row's products are its own column: rows of other adapters are left as they are, whatever
+            // this one's factors hold
+            const bool match = mine == slot[k];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (blk0 + j >= blocks) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    f4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < S; ++s)
+#pragma unroll
+                        for (int p = 0; p < P; ++p) d = mfma16<FT>(u2{b[k][j][s][2 * h], b[k][j][s][2 * h + 1]}, part[s][p], d);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[j][h][e] = match ? d[e] : acc[j][h][e];
+                }
+            }
+        }
+    }
+    if (m >= a.M) return;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t n = col(j, h);
+            f4 v = base[j][h];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = FT == kF16 ? fmaf(acc[j][h][e], inv, v[e]) : v[e] + acc[j][h][e];
+            if (a.quads) {
+                if (n < a.N) *reinterpret_cast<f4*>(a.out + m * a.N + n) = v;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < a.N) a.out[m * a.N + n + e] = v[e];
+            }
+        }
+}
+
+// One slot's factors into the set, 16 bytes a thread, and its alpha; zeros past rank, K and N.
+template <int FT, int ST>
+__global__ __launch_bounds__(256) void load_kernel(AdapterSet set, int slot, const void* A, const void* B, int rank, float alpha) {
+    const int64_t R = set.rank_tiles, a_units = set.k_pad / 32 * R * 64, b_units = set.n_pad / 32 * R * 64;
+    uint8_t* const base = set.data + slot * set.slot_bytes;
+    for (int64_t u = blockIdx.x * 256 + threadIdx.x; u < a_units + b_units; u += (int64_t)gridDim.x * 256) {
+        const bool b = u >= a_units;
+        const int64_t v = b ? u - a_units : u;
+        const int lane = (int)(v & 63), i = lane & 15, q = lane >> 4;
+        const int64_t tile = (v >> 6) % R, at = (v >> 6) / R;           // at: step of 32 columns, or block of 32 outputs
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (b) {
+                const int64_t n = 32 * at + adapter_col(i, e >> 2), r = 16 * tile + 4 * q + (e & 3);
+                f[e] = n < set.N && r < rank ? load_elem<ST>(B, n * rank + r) : 0.0f;
+            } else {
+                const int64_t r = 16 * tile + i, k = 32 * at + 8 * q + e;
+                f[e] = k < set.K && r < rank ? load_elem<ST>(A, r * set.K + k) : 0.0f;
+            }
+        }
+        u4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (FT == kF16) w[e] = bitcast<uint32_t>(h2{(_Float16)f[2 * e], (_Float16)f[2 * e + 1]});
+            else w[e] = bitcast<uint32_t>(b2{(__bf16)f[2 * e], (__bf16)f[2 * e + 1]});
+        }
+        *reinterpret_cast<u4*>(base + (b ? set.b_offset : 0) + 16 * v) = w;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) set.alpha[slot] = alpha;
+}
+
+template <int FT, int XT>
+hipError_t down_launch(const AdapterArgs& a, bool vec, dim3 grid, hipStream_t s) {
+    if (vec) hipLaunchKernelGGL((down_kernel<FT, XT, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((down_kernel<FT, XT, false>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int FT>
+hipError_t up_launch(const AdapterArgs& a, bool wide, dim3 grid, hipStream_t s) {
+#define Q4GSW_UP(S)                                                                                   \
+    case S:                                                                                           \
+        if (wide) hipLaunchKernelGGL((up_kernel<FT, S, 4>), grid, dim3(256), 0, s, a);                \
+        else hipLaunchKernelGGL((up_kernel<FT, S, 1>), grid, dim3(256), 0, s, a);                     \
+        break;
+    switch (a.rank_tiles) {
+        Q4GSW_UP(1)
+        Q4GSW_UP(2)
+        Q4GSW_UP(3)
+        Q4GSW_UP(4)
+        default: return hipErrorInvalidValue;
+    }
+#undef Q4GSW_UP
+    return hipGetLastError();
+}
+
+// How a call's work is cut.  t: enough waves to fill the GPU, but chunks of 256 columns at least and 16 of
+// them at most (the second launch reads each).  Adapters of a tile of single tokens are all unlike, those of
+// long prompts mostly one: up to 256 rows every one has waves of its own, beyond two.
+struct Cut {
+    int64_t tiles;
+    int chunks, subs, chunk_groups, groups;
+    bool wide;
+    int64_t col_groups;
+};
+Cut cut_of(const AdapterSet& set, int64_t M) {
+    Cut c;
+    c.tiles = (M + 15) / 16;
+    const int64_t most = (set.k_pad + kSub - 1) / kSub;
+    int64_t want = 2048 / (c.tiles * set.rank_tiles);
+    want = want < 1 ? 1 : (want > 16 ? 16 : want);
+    if (want > most) want = most;
+    c.subs = (int)((most + want - 1) / want);
+    c.chunks = (int)((most + c.subs - 1) / c.subs);
+    c.chunk_groups = (c.chunks + 3) / 4;
+    c.groups = M <= 256 ? (int)(M < 16 ? M : 16) : 2;
+    c.wide = c.tiles * ((set.N + 511) / 512) >= 512;
+    c.col_groups = (set.N + (c.wide ? 511 : 127)) / (c.wide ? 512 : 128);
+    return c;
+}
+
+}  // namespace
+
+bool adapters_launch_ok(const AdapterSet& set, int64_t M) {
+    const Cut c = cut_of(set, M);
+    const int64_t most = (int64_t(1) << 32) / 256 - 1;           // threads of a grid
+    return c.tiles * c.groups * set.rank_tiles <= most / c.chunk_groups && c.tiles <= most / c.col_groups;
+}
+
+uint64_t adapters_ws_bytes(const AdapterSet& set, int64_t M) {
+    return (uint64_t)cut_of(set, M).chunks * M * 16 * set.rank_tiles * 4;
+}
+
+hipError_t launch_adapters_load(const AdapterSet& set, int slot, const void* A, const void* B, int src_dtype, int rank, float alpha,
+                                hipStream_t s) {
+    const int64_t units = (set.k_pad + set.n_pad) / 32 * set.rank_tiles * 64;
+    const int64_t want = (units + 255) / 256;
+    const dim3 grid((unsigned)(want < 4096 ? want : 4096));
+#define Q4GSW_LOAD(FT, ST) hipLaunchKernelGGL((load_kernel<FT, ST>), grid, dim3(256), 0, s, set, slot, A, B, rank, alpha)
+    if (set.dtype == kF16) {
+        if (src_dtype == kF32) Q4GSW_LOAD(kF16, kF32);
+        else if (src_dtype == kF16) Q4GSW_LOAD(kF16, kF16);
+        else Q4GSW_LOAD(kF16, kBF16);
+    } else {
+        if (src_dtype == kF32) Q4GSW_LOAD(kBF16, kF32);
+        else if (src_dtype == kF16) Q4GSW_LOAD(kBF16, kF16);
+        else Q4GSW_LOAD(kBF16, kBF16);
+    }
+#undef Q4GSW_LOAD
+    return hipGetLastError();
+}
+
+hipError_t launch_adapters_add(const AdapterSet& set, const void* x, int x_dtype, int64_t M, const int32_t* slot, const float* y,
+                               float* out, void* ws, hipStream_t s) {
+    const Cut c = cut_of(set, M);
+    AdapterArgs a{set, x, M, set.K, set.N, slot, y, out, static_cast<float*>(ws), c.chunks, c.subs, c.chunk_groups, c.groups,
+                  set.rank_tiles, c.col_groups, false};
+    a.quads = set.N % 4 == 0 && ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+    const int es = x_dtype == kF32 ? 4 : 2;
+    const bool vec = (set.K * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
+    const dim3 down((unsigned)(c.tiles * c.groups * set.rank_tiles * c.chunk_groups)), up((unsigned)(c.tiles * c.col_groups));
+    hipError_t e;
+    if (set.dtype == kF16)
+        e = x_dtype == kF32 ? down_launch<kF16, kF32>(a, vec, down, s)
+                            : (x_dtype == kF16 ? down_launch<kF16, kF16>(a, vec, down, s) : down_launch<kF16, kBF16>(a, vec, down, s));
+    else
+        e = x_dtype == kF32 ? down_launch<kBF16, kF32>(a, vec, down, s)
+                            : (x_dtype == kF16 ? down_launch<kBF16, kF16>(a, vec, down, s) : down_launch<kBF16, kBF16>(a, vec, down, s));
+    if (e != hipSuccess) return e;
+    return set.dtype == kF16 ? up_launch<kF16>(a, c.wide, up, s) : up_launch<kBF16>(a, c.wide, up, s);
+}
+
+}  // namespace q4gsw

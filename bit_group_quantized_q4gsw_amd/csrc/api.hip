@@ -10,6 +10,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "adapter_set.h"
 #include "api_util.h"
 #include "internal.h"
 
@@ -291,6 +292,40 @@ void* scratch_of_current_device() {
         g_scratch_ptr[dev] = p;
     });
     return g_scratch_ptr[dev];
+}
+
+q4gsw_status set_shape(const q4gsw_adapters* a, AdapterSet* v, uint64_t* need) {
+    if (!a) return Q4GSW_E_NULL;
+    if (a->N < 1 || a->N > kMaxDim || a->K < 1 || a->K > kMaxDim || a->slots < 1 || a->slots > kAdapterSlots || a->rank < 1 ||
+        a->rank > kAdapterRank || a->reserved != 0)
+        return Q4GSW_E_SHAPE;
+    if (a->dtype != Q4GSW_F16 && a->dtype != Q4GSW_BF16) return Q4GSW_E_DTYPE;
+    *v = AdapterSet{};
+    v->N = a->N;
+    v->K = a->K;
+    v->n_pad = round_up(a->N, 32);
+    v->k_pad = round_up(a->K, 32);
+    v->slots = a->slots;
+    v->rank_tiles = (a->rank + 15) / 16;
+    v->dtype = a->dtype;
+    v->b_offset = 32 * (int64_t)v->rank_tiles * v->k_pad;
+    v->slot_bytes = v->b_offset + 32 * (int64_t)v->rank_tiles * v->n_pad;
+    // at most 2^20 slots of 2^38 bytes
+    *need = (uint64_t)v->slot_bytes * a->slots + (uint64_t)round_up(4 * (int64_t)a->slots, 256);
+    return Q4GSW_OK;
+}
+
+q4gsw_status check_set(const q4gsw_adapters* a, AdapterSet* v, Range* r) {
+    uint64_t need = 0;
+    const q4gsw_status st = set_shape(a, v, &need);
+    if (st != Q4GSW_OK) return st;
+    if (!a->data) return Q4GSW_E_NULL;
+    if (a->bytes < need) return Q4GSW_E_BUFFER;
+    if (reinterpret_cast<uintptr_t>(a->data) & 15u) return Q4GSW_E_ALIGN;
+    v->data = static_cast<uint8_t*>(a->data);
+    v->alpha = reinterpret_cast<float*>(v->data + v->slot_bytes * a->slots);
+    *r = range_of(a->data, need);
+    return Q4GSW_OK;
 }
 
 }  // namespace
@@ -858,5 +893,94 @@ const char* q4gsw_status_str(int32_t status) {
 uint32_t q4gsw_layout_version(void) { return Q4GSW_LAYOUT_VERSION; }
 
 const char* q4gsw_build_info(void) { return "q4gsw gfx950 layout-v2 built " __DATE__ " " __TIME__; }
+
+// ---- adapters of many requests ------------------------------------------------------------------
+q4gsw_status q4gsw_adapters_bytes(const q4gsw_adapters* set, uint64_t* bytes) {
+    if (!bytes) return Q4GSW_E_NULL;
+    AdapterSet v;
+    return set_shape(set, &v, bytes);
+}
+
+q4gsw_status q4gsw_adapters_load(const q4gsw_adapters* set, int32_t slot, const void* A, const void* B, int32_t src_dtype,
+                                 int32_t rank, float alpha, void* stream) {
+    AdapterSet v;
+    Range r;
+    const q4gsw_status st = check_set(set, &v, &r);
+    if (st != Q4GSW_OK) return st;
+    if (!A || !B) return Q4GSW_E_NULL;
+    if (slot < 0 || slot >= set->slots || rank < 1 || rank > set->rank || !finite_f(alpha)) return Q4GSW_E_SHAPE;
+    if (!act_dtype_ok(src_dtype)) return Q4GSW_E_DTYPE;
+    if (overlap(r, range_of(A, (uint64_t)rank * set->K * esize(src_dtype))) ||
+        overlap(r, range_of(B, (uint64_t)rank * set->N * esize(src_dtype))))
+        return Q4GSW_E_ALIAS;
+    return hip_status(launch_adapters_load(v, slot, A, B, src_dtype, rank, alpha, static_cast<hipStream_t>(stream)));
+}
+
+q4gsw_status q4gsw_adapters_workspace_bytes(const q4gsw_adapters* set, const q4gsw_weight* w, int64_t M, int32_t x_dtype,
+                                            uint64_t* bytes) {
+    if (!bytes) return Q4GSW_E_NULL;
+    AdapterSet v;
+    uint64_t need = 0;
+    q4gsw_status st = set_shape(set, &v, &need);
+    if (st != Q4GSW_OK) return st;
+    if (M < 1 || M > kMaxM || !adapters_launch_ok(v, M)) return Q4GSW_E_SHAPE;
+    if (!act_dtype_ok(x_dtype)) return Q4GSW_E_DTYPE;
+    uint64_t base = 0;
+    if (w) {
+        if ((st = check_desc(w)) != Q4GSW_OK) return st;
+        if (w->N != v.N || w->K != v.K) return Q4GSW_E_SHAPE;
+        const int32_t route = pick_fwd(w, M, x_dtype, false, Q4GSW_ROUTE_NONE, &st);
+        if (st != Q4GSW_OK) return st;
+        base = fwd_ws_bytes(w, M, x_dtype, route, Opts());
+    }
+    // the linear's workspace is free again when the adapters' launches begin
+    *bytes = adapters_ws_bytes(v, M);
+    if (base > *bytes) *bytes = base;
+    return Q4GSW_OK;
+}
+
+q4gsw_status q4gsw_adapters_add(const q4gsw_adapters* set, const void* x, int32_t x_dtype, int64_t M, const int32_t* slot,
+                                const float* y, float* out, void* ws, uint64_t ws_bytes, void* stream) {
+    AdapterSet v;
+    Range sr;
+    const q4gsw_status st = check_set(set, &v, &sr);
+    if (st != Q4GSW_OK) return st;
+    if (!x || !slot || !y || !out) return Q4GSW_E_NULL;
+    if (M < 1 || M > kMaxM || !adapters_launch_ok(v, M)) return Q4GSW_E_SHAPE;
+    if (!act_dtype_ok(x_dtype)) return Q4GSW_E_DTYPE;
+    const uint64_t need = adapters_ws_bytes(v, M);
+    if (!ws_ok(ws, ws_bytes, need)) return Q4GSW_E_WORKSPACE;
+    const Range outr = range_of(out, (uint64_t)M * v.N * 4), wr = range_of(ws, need);
+    const Range ins[4] = {range_of(y, (uint64_t)M * v.N * 4), range_of(x, (uint64_t)M * v.K * esize(x_dtype)),
+                          range_of(slot, (uint64_t)M * 4), sr};
+    for (int i = 0; i < 4; ++i) {
+        if (overlap(wr, ins[i])) return Q4GSW_E_ALIAS;
+        if (overlap(outr, ins[i]) && !(i == 0 && out == y)) return Q4GSW_E_ALIAS;      // y updated in place
+    }
+    if (overlap(outr, wr)) return Q4GSW_E_ALIAS;
+    return hip_status(launch_adapters_add(v, x, x_dtype, M, slot, y, out, ws, static_cast<hipStream_t>(stream)));
+}
+
+q4gsw_status q4gsw_adapters_fwd(const q4gsw_weight* w, const q4gsw_adapters* set, const void* x, int32_t x_dtype, int64_t M,
+                                const int32_t* slot, float* y, void* ws, uint64_t ws_bytes, void* stream) {
+    const Opts o;
+    int32_t route = Q4GSW_ROUTE_NONE;
+    uint64_t base = 0;
+    q4gsw_status st = prepare_fwd(w, x, x_dtype, M, y, o, &route, &base);
+    if (st != Q4GSW_OK) return st;
+    AdapterSet v;
+    Range sr;
+    if ((st = check_set(set, &v, &sr)) != Q4GSW_OK) return st;
+    if (!slot) return Q4GSW_E_NULL;
+    if (w->N != v.N || w->K != v.K || !adapters_launch_ok(v, M)) return Q4GSW_E_SHAPE;
+    const uint64_t terms = adapters_ws_bytes(v, M), need = base > terms ? base : terms;
+    if (!ws_ok(ws, ws_bytes, need)) return Q4GSW_E_WORKSPACE;
+    if ((st = fwd_alias(w, x, x_dtype, M, y, ws, need)) != Q4GSW_OK) return st;
+    const Range yr = range_of(y, (uint64_t)M * w->N * 4), wr = range_of(ws, need), ir = range_of(slot, (uint64_t)M * 4);
+    if (overlap(yr, sr) || overlap(wr, sr) || overlap(yr, ir) || overlap(wr, ir)) return Q4GSW_E_ALIAS;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if ((st = run_fwd(w, x, x_dtype, M, y, ws, route, o, s)) != Q4GSW_OK) return st;
+    return hip_status(launch_adapters_add(v, x, x_dtype, M, slot, y, y, ws, s));
+}
 
 }  // extern "C"

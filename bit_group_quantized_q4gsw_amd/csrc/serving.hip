@@ -3,6 +3,7 @@
 #include "api_util.h"
 #include "internal.h"
 #include "kv_attention.h"
+#include "logits.h"
 
 using namespace q4gsw;
 
@@ -459,6 +460,42 @@ q4gsw_status q4gsw_kv_keep(const q4gsw_kv_cache* caches, int32_t count, const q4
             if (overlap(cr[i], cr[j])) return Q4GSW_E_ALIAS;
     }
     return hip_status(launch_kv_keep(cv, count, sv, parents, leaf, max_new, kept, path, static_cast<hipStream_t>(stream)));
+}
+
+q4gsw_status q4gsw_logits_adjust(const void* logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                 const q4gsw_logits_rules* r, void* out, int64_t out_ld, void* stream) {
+    if (!r) return Q4GSW_E_NULL;
+    if (rows < 0 || rows > kMaxM || vocab < 1 || vocab > kMaxDim || ld < vocab || out_ld < vocab || ld > kMaxDim || out_ld > kMaxDim)
+        return Q4GSW_E_SHAPE;
+    if (!act_dtype_ok(dtype)) return Q4GSW_E_DTYPE;
+    if (r->batch < 1 || r->batch > (1 << 20)) return rows == 0 && r->batch == 0 ? Q4GSW_OK : Q4GSW_E_SHAPE;
+    if (!r->cu && r->batch != rows) return Q4GSW_E_SHAPE;
+    if (r->max_new < 1 || r->max_new > (r->parents ? kTreeMax : kMaxM)) return Q4GSW_E_SHAPE;
+    if (r->parents && (!r->cu || !r->ids)) return Q4GSW_E_NULL;
+    if (r->history && (r->history_cols < 0 || r->history_ld < r->history_cols || r->history_ld > kMaxDim)) return Q4GSW_E_SHAPE;
+    if (r->history && !r->history_len) return Q4GSW_E_NULL;
+    if (r->bias_ids && (r->bias_cols < 0 || r->bias_ld < r->bias_cols || r->bias_ld > kMaxDim)) return Q4GSW_E_SHAPE;
+    if (r->bias_ids && !r->bias) return Q4GSW_E_NULL;
+    if (r->mask && (r->mask_ld < (vocab + 31) / 32 || r->mask_ld > kMaxDim)) return Q4GSW_E_SHAPE;
+    if (rows == 0) return Q4GSW_OK;
+    if (!logits || !out) return Q4GSW_E_NULL;
+    LogitsArgs a{logits, out, rows, vocab, ld, out_ld, r->batch, r->max_new, r->cu, r->history, r->history_ld, r->history_cols,
+                 r->history_len, r->prompt_len, r->ids, r->parents, r->repetition, r->presence, r->frequency, r->bias_ids,
+                 r->bias, r->bias_ld, r->bias_cols, r->mask, r->mask_ld, 0, 0, false};
+    if (!r->history) a.prompt_len = nullptr;
+    if (!logits_launch_ok(a)) return Q4GSW_E_SHAPE;
+    const int es = esize(dtype);
+    const uint64_t B = (uint64_t)r->batch;
+    const Range outr = range_of(out, rows_extent(rows, out_ld, vocab, es));
+    auto hit = [&](const void* p, uint64_t bytes) { return p && overlap(outr, range_of(p, bytes)); };
+    if (!(out == logits && out_ld == ld) && hit(logits, rows_extent(rows, ld, vocab, es))) return Q4GSW_E_ALIAS;
+    if (hit(r->cu, (B + 1) * 4) || hit(r->history, rows_extent(r->batch, r->history_ld, r->history_cols, 4)) ||
+        hit(r->history_len, B * 4) || hit(r->prompt_len, B * 4) || hit(r->ids, rows * 4) || hit(r->parents, rows * 4) ||
+        hit(r->repetition, B * 4) || hit(r->presence, B * 4) || hit(r->frequency, B * 4) ||
+        hit(r->bias_ids, rows_extent(r->batch, r->bias_ld, r->bias_cols, 4)) ||
+        hit(r->bias, rows_extent(r->batch, r->bias_ld, r->bias_cols, 4)) || hit(r->mask, rows_extent(rows, r->mask_ld, (vocab + 31) / 32, 4)))
+        return Q4GSW_E_ALIAS;
+    return hip_status(launch_logits(a, dtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -349,6 +349,57 @@ q4gsw_status q4gsw_adamw_step(float *param, const float *grad, float *exp_avg, f
                               const q4gsw_adamw_params *hp, int64_t step, void *stream);
 
 /*
+ * Adapters of many requests beside one projection, for serving: row m of a call takes the adapter of slot
+ * slot[m] of a set,
+ *   out[m] = y[m] + alpha_s (x[m] A_s^T) B_s^T,  s = slot[m],  A_s [rank, K], B_s [N, rank].
+ * A set is plain data, filled by the caller; `data` (16-byte aligned, q4gsw_adapters_bytes bytes) stays the
+ * caller's.  q4gsw_adapters_load writes one slot (factors of any rank up to the set's, each rounded once to
+ * the set's type, and a finite alpha); a slot that was never loaded gives zeros if its bytes are
+ * zeros.  slot[m] outside [0, slots): no adapter, out[m] = y[m].
+ */
+typedef struct q4gsw_adapters {
+    int64_t N, K;
+    int32_t slots;            /* 1..2^20 */
+    int32_t rank;             /* the largest: 1..64 */
+    int32_t dtype;            /* of the factors as held: Q4GSW_F16 or Q4GSW_BF16 */
+    int32_t reserved;         /* 0 */
+    void *data;
+    uint64_t bytes;
+} q4gsw_adapters;
+/* Bytes of a set (data and bytes of `set` are not looked at).  E_NULL, E_SHAPE, E_DTYPE. */
+q4gsw_status q4gsw_adapters_bytes(const q4gsw_adapters *set, uint64_t *bytes);
+/*
+ *   A device [rank, K], B device [N, rank], both in src_dtype
+ * E_NULL, E_SHAPE (slot, rank, alpha not finite), E_DTYPE, E_BUFFER, E_ALIGN, E_ALIAS (a factor overlaps the
+ * set), E_HIP.
+ */
+q4gsw_status q4gsw_adapters_load(const q4gsw_adapters *set, int32_t slot, const void *A, const void *B,
+                                 int32_t src_dtype, int32_t rank, float alpha, void *stream);
+/* Workspace of q4gsw_adapters_fwd with this weight, or of q4gsw_adapters_add (w NULL).
+ * E_NULL, E_SHAPE (M; w's shape is not the set's), E_DTYPE, E_DESC, E_GROUP. */
+q4gsw_status q4gsw_adapters_workspace_bytes(const q4gsw_adapters *set, const q4gsw_weight *w, int64_t M,
+                                            int32_t x_dtype, uint64_t *bytes);
+/*
+ * q4gsw_adapters_add: beside a projection that was computed otherwise (int8 rows, one of a fused QKV).
+ *   x    device [M, K] in x_dtype;  slot device int32 [M]
+ *   y    device fp32 [M, N];  out device fp32 [M, N] (written), may be y itself
+ *   ws   device workspace of ws_bytes >= q4gsw_adapters_workspace_bytes (256-byte aligned)
+ * q4gsw_adapters_fwd: with the 4-bit linear as the projection, y[m] = x[m] . dequant(W)^T + the adapter's
+ * term (q4gsw_linear_fwd's routes and precision).
+ * Factors are used as held; x and x A^T enter their products with 22 bits or more, relative to the row's
+ * largest where the factors are fp16 and the type is another; all sums are fp32, in an order that depends
+ * on the sizes alone.  A row of x that is not finite gives values that are not finite, in that row alone.
+ * E_NULL, E_SHAPE (M, or w's shape is not the set's), E_DTYPE, E_DESC, E_GROUP, E_BUFFER, E_ALIGN, E_WORKSPACE,
+ * E_ALIAS (an output or ws overlaps an input, the set or each other), E_HIP.
+ */
+q4gsw_status q4gsw_adapters_add(const q4gsw_adapters *set, const void *x, int32_t x_dtype, int64_t M,
+                                const int32_t *slot, const float *y, float *out, void *ws, uint64_t ws_bytes,
+                                void *stream);
+q4gsw_status q4gsw_adapters_fwd(const q4gsw_weight *w, const q4gsw_adapters *set, const void *x, int32_t x_dtype,
+                                int64_t M, const int32_t *slot, float *y, void *ws, uint64_t ws_bytes,
+                                void *stream);
+
+/*
  * Embedding row gather: out[t, k] = dequant(W)[ids[t], k], for t < T and k < K.
  * The embedding_q4gsw op of the Gemma 4 ExecuTorch export (maintainer comment on the
  * react-native-executorch issue "Upstream the Gemma 4 Vulkan support we carry on our
@@ -555,6 +606,58 @@ q4gsw_status q4gsw_kv_tree_attention_ex(const q4gsw_kv_cache *c, const q4gsw_kv_
 q4gsw_status q4gsw_kv_keep(const q4gsw_kv_cache *caches, int32_t count, const q4gsw_kv_seqs *s,
                            const int32_t *parents, const int32_t *leaf, int32_t max_new, int32_t *kept,
                            int32_t *path, void *stream);
+
+/*
+ * Rules on logits before a token is chosen, every step in fp32 as written, for row l of V logits:
+ *   x = l[v];
+ *   v seen so far:               x = x > 0 ? x / repetition : x * repetition
+ *   v generated n > 0 times:     x = (x - frequency * n) - presence
+ *   v biased:                    x = x + bias
+ *   v masked:                    x = -inf
+ * and one rounding to the logits' type.  A mask that leaves nothing gives a row of -inf.
+ * Rows belong to sequences as in q4gsw_kv_seqs: cu[b] .. cu[b + 1] - 1 to sequence b, or row r to sequence r
+ * (cu NULL, batch rows).  Rows of no sequence, and rows of a sequence past max_new, are not touched.
+ *   history      device int32 [batch][history_ld >= history_cols], or NULL: the first history_len[b] (device
+ *                int32 [batch]; at most history_cols) entries of row b are the tokens sequence b has behind it,
+ *                of which the first prompt_len[b] (device int32 [batch]; NULL: none) are seen but not generated
+ *   ids          device int32 [rows], or NULL: the tokens of the rows themselves.  A row has seen and
+ *                generated its own token and those of the rows of its sequence before it, or with
+ *   parents      (device int32 [rows], as in q4gsw_kv_tree_attention; needs cu, ids and max_new at most 512)
+ *                those of its ancestors only
+ *   repetition, presence, frequency   device fp32 [batch], or NULL: 1, 0 and 0
+ *   bias_ids     device int32 [batch][bias_ld >= bias_cols], or NULL, with bias, device fp32 of the same shape:
+ *                of entries with one token the last counts
+ *   mask         device [rows][mask_ld >= ceil(V / 32)], or NULL: bit v % 32 of word v / 32 allows token v
+ * Tokens outside [0, V) count for nothing.
+ */
+typedef struct q4gsw_logits_rules {
+    int32_t batch;
+    int32_t max_new;
+    const int32_t *cu;
+    const int32_t *history;
+    int64_t history_ld;
+    int32_t history_cols;
+    int32_t bias_cols;
+    const int32_t *history_len;
+    const int32_t *prompt_len;
+    const int32_t *ids;
+    const int32_t *parents;
+    const float *repetition;
+    const float *presence;
+    const float *frequency;
+    const int32_t *bias_ids;
+    const float *bias;
+    int64_t bias_ld;
+    const uint32_t *mask;
+    int64_t mask_ld;
+} q4gsw_logits_rules;
+/*
+ *   logits  device, rows `ld` elements apart, in dtype;  out  device, rows out_ld elements apart, in dtype:
+ *           may be logits itself (out_ld then ld)
+ * E_NULL, E_SHAPE, E_DTYPE, E_ALIAS (out overlaps an input), E_HIP.  Rows of 0 launch nothing.
+ */
+q4gsw_status q4gsw_logits_adjust(const void *logits, int32_t dtype, int64_t rows, int64_t V, int64_t ld,
+                                 const q4gsw_logits_rules *rules, void *out, int64_t out_ld, void *stream);
 
 /* Route attestation: the q4gsw_route_id a plain call (no options) with these
  * arguments takes (Q4GSW_ROUTE_NONE if it would fail validation).  For
