@@ -33,9 +33,9 @@ struct AdapterArgs {
     const int32_t* slot;
     const float* y;
     float* out;
-    float* part;             // [chunk][M][16 rank_tiles]
-    int chunks, subs;        // of K; runs of 256 columns in a chunk
-    int chunk_groups, groups;
+    float* t;                // [chunk][M][16 rank_tiles]
+    int chunks;              // of K
+    int groups;              // workgroups that share a tile's adapters in the first launch
     int rank_tiles;
     int64_t col_groups;
     bool quads;              // rows of y and out hold aligned quads

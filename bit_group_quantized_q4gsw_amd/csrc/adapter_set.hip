@@ -4,12 +4,13 @@
 //
 // A set holds its slots' factors in 16 bits, laid out when a slot is loaded for the matrix operands that
 // read them (adapter_set.h), so odd ranks, widths and alignments cost nothing later.  Two launches:
-//   * t[m] = x[m] A_s^T, K cut into chunks: a wave takes 16 rows, one of the adapters among them, 16 ranks
-//     and one chunk; factors as the first operand of the 16x16x32 product, rows as the second.  Rows of
-//     other adapters are not loaded: they are zeros there, and their columns of the product are not stored;
-//   * out = y + alpha t B_s^T: a workgroup adds the chunks' t once (in a fixed order), and its waves walk the
-//     adapters of the 16 rows; factors as the first operand of the 16x16x16 product, so that a lane ends
-//     with eight neighbouring columns of one row.
+//   * t[m] = x[m] A_s^T: a workgroup takes 16 rows, one or more of the adapters among them and 16 ranks;
+//     its waves share K and add up in LDS.  Factors are the first operand of the 16x16x32 product, rows the
+//     second.  Rows of other adapters are not loaded: they are zeros there, and their columns of the product are
+//     not stored;
+//   * out = y + alpha t B_s^T: factors as the first operand of the 16x16x16 product, so that a lane ends
+//     with eight neighbouring columns of one row.  With few rows the waves of a workgroup share the adapters of
+//     16 rows (a row is its adapter's wave's alone), with many they share the columns.
 // Rows need no order: adapters are found among each 16 rows by comparison, and one that many tiles share
 // is read from L2 by all but the first.
 //
@@ -24,8 +25,6 @@
 
 namespace q4gsw {
 namespace {
-
-constexpr int kSub = 256;            // columns of x loaded at a time: 8 steps of 32
 
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
@@ -109,45 +108,49 @@ struct Octet {
     }
 };
 
-// t of 16 rows, 16 ranks and one chunk, a wave: part[chunk][m][rank].
+constexpr int kWaves = 8;                // of a workgroup, which share a chunk of K
+constexpr int kMostChunks = 4;
+
+// t of 16 rows, 16 ranks and a chunk of K: t[chunk][m][rank].
 template <int FT, int XT, bool VEC>
-__global__ __launch_bounds__(256) void down_kernel(AdapterArgs a) {
+__global__ __launch_bounds__(64 * kWaves) void down_kernel(AdapterArgs a) {
     constexpr int P = row_parts<FT, XT>();
     constexpr bool SCALED = FT == kF16 && XT != kF16;
-    constexpr int kSteps = kSub / 32;
-    const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kSteps = 8;                             // of 32 columns, loaded together
+    __shared__ f4 s_sum[kWaves][64];
+    const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int64_t id = blockIdx.x;
-    const int chunk = (int)(id % a.chunk_groups) * 4 + wave;
-    id /= a.chunk_groups;
+    const int chunk = (int)(id % a.chunks);
+    id /= a.chunks;
     const int rt = (int)(id % a.rank_tiles);
     id /= a.rank_tiles;
     const int group = (int)(id % a.groups);
     const int64_t tile = id / a.groups;
-    if (chunk >= a.chunks) return;
     const int mine = row_slot(a, tile, i);
     uint32_t firsts = first_rows(mine, i);
     const int64_t m = 16 * tile + i, row = m * a.K;
-    const int64_t steps = a.set.k_pad >> 5;
+    const int64_t steps = a.set.k_pad >> 5, parts = a.chunks * kWaves, per = (steps + parts - 1) / parts;
+    const int64_t begin = per * (chunk * kWaves + wave), s1 = min(begin + per, steps);
     for (int n = 0; firsts; firsts &= firsts - 1, ++n) {
         if (n % a.groups != group) continue;
         const int slot = __builtin_amdgcn_readlane(mine, __builtin_ctz(firsts));
         const bool match = mine == slot;
         const uint8_t* A = a.set.data + slot * a.set.slot_bytes + 1024 * (int64_t)rt + 16 * lane;
         f4 sum = {0.f, 0.f, 0.f, 0.f};
-        for (int sub = 0; sub < a.subs; ++sub) {
-            const int64_t s0 = ((int64_t)chunk * a.subs + sub) * kSteps;
+        for (int64_t s0 = begin; s0 < s1; s0 += kSteps) {
             u4 av[kSteps];
             Octet<XT, VEC> xv[kSteps];
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 av[s] = u4{0u, 0u, 0u, 0u};
                 xv[s].clear();
-                if (s0 + s < steps) av[s] = ldg16(A + (s0 + s) * a.rank_tiles * 1024);
+                if (s0 + s < s1) av[s] = ldg16(A + (s0 + s) * a.rank_tiles * 1024);
             }
             if (match) {
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s) xv[s].load(a.x, row, 32 * (s0 + s) + 8 * q, a.K);
+                for (int s = 0; s < kSteps; ++s)
+                    if (s0 + s < s1) xv[s].load(a.x, row, 32 * (s0 + s) + 8 * q, a.K);
             }
             float mul = 1.0f, inv = 1.0f;
             if constexpr (SCALED) {
@@ -183,26 +186,67 @@ __global__ __launch_bounds__(256) void down_kernel(AdapterArgs a) {
             for (int e = 0; e < 4; ++e) sum[e] = SCALED ? fmaf(acc[e], inv, sum[e]) : sum[e] + acc[e];
         }
         // lane (i, q) holds ranks 4 q .. + 3 of row i
-        if (match) *reinterpret_cast<f4*>(a.part + (chunk * a.M + m) * (16 * a.rank_tiles) + 16 * rt + 4 * q) = sum;
+        s_sum[wave][lane] = sum;
+        __syncthreads();
+        if (tid < 256) {
+            const int l = tid >> 2, e = tid & 3, ri = l & 15;
+            float t = s_sum[0][l][e];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) t += s_sum[w][l][e];
+            if (__shfl(mine, ri) == slot) a.t[(chunk * a.M + 16 * tile + ri) * (16 * a.rank_tiles) + 16 * rt + 4 * (l >> 4) + e] = t;
+        }
+        __syncthreads();
     }
 }
 
-// out = y + alpha t B^T for 16 rows and 128 J columns, S steps of 16 ranks.
-template <int FT, int S, int J>
+// out = y + alpha t B^T for 16 rows, S steps of 16 ranks.  MANY: 256 columns, 64 a wave; else 32 J columns,
+// every fourth adapter of the rows a wave.
+template <int FT, int S, bool MANY>
 __global__ __launch_bounds__(256) void up_kernel(AdapterArgs a) {
-    constexpr int G = S == 1 ? 4 : (S == 2 ? 2 : 1);      // groups of threads that add t's chunks
-    constexpr int kBatch = J * S <= 4 ? 4 : 1;            // adapters whose factors are loaded together
+    constexpr int J = MANY || S == 1 ? 2 : 1;             // blocks of 32 columns a wave
+    constexpr int kBatch = MANY ? 1 : 4;                  // adapters whose factors are loaded together
     constexpr int P = FT == kF16 ? 2 : 3;
-    __shared__ f4 s_t[G][64 * S];
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t tile = blockIdx.x / a.col_groups, m = 16 * tile + i;
-    const int64_t blk0 = (int64_t)(blockIdx.x % a.col_groups) * 4 * J + wave * J;
+    const int64_t blk0 = (int64_t)(blockIdx.x % a.col_groups) * (MANY ? 4 * J : J) + (MANY ? wave * J : 0);
+    const int64_t blocks = a.set.n_pad >> 5;
+    if (MANY && blk0 >= blocks) return;
     const int mine = row_slot(a, tile, i);
     uint32_t firsts = first_rows(mine, i);
-    if (!firsts && a.y == a.out) return;
+    bool here = m < a.M && (mine >= 0 || a.y != a.out);   // rows that this wave writes
+    if constexpr (!MANY) {
+        uint32_t left = firsts;
+        firsts = 0;
+        here = here && mine < 0 && wave == 0;
+        for (int n = 0; left; left &= left - 1, ++n) {
+            if ((n & 3) != wave) continue;
+            firsts |= left & (0u - left);
+            here |= mine == __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
+        }
+        if (!__any(here)) return;
+    }
 
-    // what the columns hold so far
+    // t and what the columns hold so far
+    f4 tv[S];
+    float alpha = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) tv[s] = f4{0.f, 0.f, 0.f, 0.f};
+    if (here && mine >= 0) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const float* t = a.t + m * (16 * S) + 16 * s + 4 * q;
+            f4 v[kMostChunks];
+#pragma unroll
+            for (int c = 0; c < kMostChunks; ++c) v[c] = *reinterpret_cast<const f4*>(t + min(c, a.chunks - 1) * a.M * (16 * S));
+            tv[s] = v[0];
+#pragma unroll
+            for (int c = 1; c < kMostChunks; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tv[s][e] += c < a.chunks ? v[c][e] : 0.0f;
+        }
+        alpha = a.set.alpha[mine];
+    }
     f4 acc[J][2], base[J][2];
     auto col = [&](int j, int h) -> int64_t { return 32 * (blk0 + j) + 8 * q + 4 * h; };
 #pragma unroll
@@ -211,7 +255,7 @@ __global__ __launch_bounds__(256) void up_kernel(AdapterArgs a) {
         for (int h = 0; h < 2; ++h) {
             acc[j][h] = base[j][h] = f4{0.f, 0.f, 0.f, 0.f};
             const int64_t n = col(j, h);
-            if (m < a.M) {
+            if (here) {
                 if (a.quads) {
                     if (n < a.N) base[j][h] = *reinterpret_cast<const f4*>(a.y + m * a.N + n);
                 } else {
@@ -221,44 +265,31 @@ __global__ __launch_bounds__(256) void up_kernel(AdapterArgs a) {
                 }
             }
         }
-
-    // t of the 16 rows: thread (g, s, q, i) adds every G-th chunk of four ranks of a row
-    const int g = tid / (64 * S);
-    if (g < G) {
-        const int s = (tid / 64) % S;
-        f4 t = {0.f, 0.f, 0.f, 0.f};
-        if (mine >= 0) {
-            const int64_t at = m * (16 * S) + 16 * s + 4 * q;
-            constexpr int kLoads = 4;
-            for (int c0 = g; c0 < a.chunks; c0 += kLoads * G) {
-                f4 v[kLoads];
+    u4 b[kBatch][J][S];
+    int slot[kBatch];
+    auto fetch = [&]() {
 #pragma unroll
-                for (int k = 0; k < kLoads; ++k) {
-                    const int c = c0 + k * G;
-                    v[k] = *reinterpret_cast<const f4*>(a.part + (c < a.chunks ? c : c0) * a.M * (16 * S) + at);
-                }
+        for (int k = 0; k < kBatch; ++k) {
+            slot[k] = -1;
+            if (!firsts) continue;
+            slot[k] = __builtin_amdgcn_readlane(mine, __builtin_ctz(firsts));
+            firsts &= firsts - 1;
+            const uint8_t* B = a.set.data + slot[k] * a.set.slot_bytes + a.set.b_offset + 16 * lane;
 #pragma unroll
-                for (int k = 0; k < kLoads; ++k) {
-                    if (c0 + k * G >= a.chunks) break;
+            for (int j = 0; j < J; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) t[e] += v[k][e];
-                }
-            }
+                for (int s = 0; s < S; ++s)
+                    if (blk0 + j < blocks) b[k][j][s] = ldg16(B + ((blk0 + j) * S + s) * 1024);
         }
-        s_t[g][64 * s + lane] = t;
-    }
-    const float alpha = mine >= 0 ? a.set.alpha[mine] : 0.0f;
-    __syncthreads();
-    float tv[S][4];
+    };
+    fetch();
+
     float amax = 0.0f;
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            float v = s_t[0][64 * s + lane][e];
-#pragma unroll
-            for (int k = 1; k < G; ++k) v += s_t[k][64 * s + lane][e];
-            tv[s][e] = v * alpha;
+            tv[s][e] *= alpha;
             amax = fmaxf(amax, fabsf(tv[s][e]));
         }
     float mul = 1.0f, inv = 1.0f;
@@ -273,23 +304,7 @@ __global__ __launch_bounds__(256) void up_kernel(AdapterArgs a) {
             for (int p = 0; p < P; ++p) part[s][p][e] = take_part<FT>(v0, v1);
         }
 
-    const int64_t blocks = a.set.n_pad >> 5;
-    while (firsts) {
-        int slot[kBatch];
-        u4 b[kBatch][J][S];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            slot[k] = -1;
-            if (!firsts) continue;
-            slot[k] = __builtin_amdgcn_readlane(mine, __builtin_ctz(firsts));
-            firsts &= firsts - 1;
-            const uint8_t* B = a.set.data + slot[k] * a.set.slot_bytes + a.set.b_offset + 16 * lane;
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int s = 0; s < S; ++s)
-                    if (blk0 + j < blocks) b[k][j][s] = ldg16(B + ((blk0 + j) * S + s) * 1024);
-        }
+    for (; slot[0] >= 0; fetch()) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             if (slot[k] < 0) break;
@@ -312,7 +327,7 @@ __global__ __launch_bounds__(256) void up_kernel(AdapterArgs a) {
             }
         }
     }
-    if (m >= a.M) return;
+    if (!here) return;
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -364,18 +379,18 @@ __global__ __launch_bounds__(256) void load_kernel(AdapterSet set, int slot, con
 }
 
 template <int FT, int XT>
-hipError_t down_launch(const AdapterArgs& a, bool vec, dim3 grid, hipStream_t s) {
-    if (vec) hipLaunchKernelGGL((down_kernel<FT, XT, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((down_kernel<FT, XT, false>), grid, dim3(256), 0, s, a);
+hipError_t down_launch(const AdapterArgs& a, bool vec, dim3 grid, dim3 block, hipStream_t s) {
+    if (vec) hipLaunchKernelGGL((down_kernel<FT, XT, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((down_kernel<FT, XT, false>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
 template <int FT>
-hipError_t up_launch(const AdapterArgs& a, bool wide, dim3 grid, hipStream_t s) {
+hipError_t up_launch(const AdapterArgs& a, bool many, dim3 grid, hipStream_t s) {
 #define Q4GSW_UP(S)                                                                                   \
     case S:                                                                                           \
-        if (wide) hipLaunchKernelGGL((up_kernel<FT, S, 4>), grid, dim3(256), 0, s, a);                \
-        else hipLaunchKernelGGL((up_kernel<FT, S, 1>), grid, dim3(256), 0, s, a);                     \
+        if (many) hipLaunchKernelGGL((up_kernel<FT, S, true>), grid, dim3(256), 0, s, a);             \
+        else hipLaunchKernelGGL((up_kernel<FT, S, false>), grid, dim3(256), 0, s, a);                 \
         break;
     switch (a.rank_tiles) {
         Q4GSW_UP(1)
@@ -388,28 +403,24 @@ hipError_t up_launch(const AdapterArgs& a, bool wide, dim3 grid, hipStream_t s) 
     return hipGetLastError();
 }
 
-// How a call's work is cut.  t: enough waves to fill the GPU, but chunks of 256 columns at least and 16 of
-// them at most (the second launch reads each).  Adapters of a tile of single tokens are all unlike, those of
-// long prompts mostly one: up to 256 rows every one has waves of its own, beyond two.
+// How a call's work is cut.  Adapters of a tile of single tokens are all unlike, those of long prompts
+// mostly one: up to 256 rows every one has workgroups of its own, beyond that two share them.  A chunk is 2048
+// columns, so that a wave has all of its loads on their way at once or twice, unless rows fill the GPU.
 struct Cut {
     int64_t tiles;
-    int chunks, subs, chunk_groups, groups;
-    bool wide;
+    int chunks, groups;
+    bool many;
     int64_t col_groups;
 };
 Cut cut_of(const AdapterSet& set, int64_t M) {
     Cut c;
     c.tiles = (M + 15) / 16;
-    const int64_t most = (set.k_pad + kSub - 1) / kSub;
-    int64_t want = 2048 / (c.tiles * set.rank_tiles);
-    want = want < 1 ? 1 : (want > 16 ? 16 : want);
-    if (want > most) want = most;
-    c.subs = (int)((most + want - 1) / want);
-    c.chunks = (int)((most + c.subs - 1) / c.subs);
-    c.chunk_groups = (c.chunks + 3) / 4;
+    const int64_t steps = set.k_pad / 32;
+    c.chunks = (int)(c.tiles >= 1024 || steps <= 64 ? 1 : (steps >= 64 * kMostChunks ? kMostChunks : (steps + 63) / 64));
     c.groups = M <= 256 ? (int)(M < 16 ? M : 16) : 2;
-    c.wide = c.tiles * ((set.N + 511) / 512) >= 512;
-    c.col_groups = (set.N + (c.wide ? 511 : 127)) / (c.wide ? 512 : 128);
+    c.many = c.tiles * ((set.N + 255) / 256) >= 1024;
+    const int cols = c.many ? 256 : (set.rank_tiles == 1 ? 64 : 32);
+    c.col_groups = (set.N + cols - 1) / cols;
     return c;
 }
 
@@ -417,8 +428,8 @@ Cut cut_of(const AdapterSet& set, int64_t M) {
 
 bool adapters_launch_ok(const AdapterSet& set, int64_t M) {
     const Cut c = cut_of(set, M);
-    const int64_t most = (int64_t(1) << 32) / 256 - 1;           // threads of a grid
-    return c.tiles * c.groups * set.rank_tiles <= most / c.chunk_groups && c.tiles <= most / c.col_groups;
+    const int64_t most = (int64_t(1) << 32) - 1;                 // threads of a grid
+    return c.tiles * c.groups * set.rank_tiles <= most / (64 * kWaves * c.chunks) && c.tiles <= most / 256 / c.col_groups;
 }
 
 uint64_t adapters_ws_bytes(const AdapterSet& set, int64_t M) {
@@ -447,21 +458,20 @@ hipError_t launch_adapters_load(const AdapterSet& set, int slot, const void* A, 
 hipError_t launch_adapters_add(const AdapterSet& set, const void* x, int x_dtype, int64_t M, const int32_t* slot, const float* y,
                                float* out, void* ws, hipStream_t s) {
     const Cut c = cut_of(set, M);
-    AdapterArgs a{set, x, M, set.K, set.N, slot, y, out, static_cast<float*>(ws), c.chunks, c.subs, c.chunk_groups, c.groups,
-                  set.rank_tiles, c.col_groups, false};
+    AdapterArgs a{set, x, M, set.K, set.N, slot, y, out, static_cast<float*>(ws), c.chunks, c.groups, set.rank_tiles, c.col_groups, false};
     a.quads = set.N % 4 == 0 && ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
     const int es = x_dtype == kF32 ? 4 : 2;
     const bool vec = (set.K * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
-    const dim3 down((unsigned)(c.tiles * c.groups * set.rank_tiles * c.chunk_groups)), up((unsigned)(c.tiles * c.col_groups));
+    const dim3 down((unsigned)(c.tiles * c.groups * set.rank_tiles * c.chunks)), block(64 * kWaves), up((unsigned)(c.tiles * c.col_groups));
     hipError_t e;
-    if (set.dtype == kF16)
-        e = x_dtype == kF32 ? down_launch<kF16, kF32>(a, vec, down, s)
-                            : (x_dtype == kF16 ? down_launch<kF16, kF16>(a, vec, down, s) : down_launch<kF16, kBF16>(a, vec, down, s));
-    else
-        e = x_dtype == kF32 ? down_launch<kBF16, kF32>(a, vec, down, s)
-                            : (x_dtype == kF16 ? down_launch<kBF16, kF16>(a, vec, down, s) : down_launch<kBF16, kBF16>(a, vec, down, s));
+#define Q4GSW_DOWN(FT)                                                                                        \
+    x_dtype == kF32 ? down_launch<FT, kF32>(a, vec, down, block, s)                                           \
+                    : (x_dtype == kF16 ? down_launch<FT, kF16>(a, vec, down, block, s) : down_launch<FT, kBF16>(a, vec, down, block, s))
+    if (set.dtype == kF16) e = Q4GSW_DOWN(kF16);
+    else e = Q4GSW_DOWN(kBF16);
+#undef Q4GSW_DOWN
     if (e != hipSuccess) return e;
-    return set.dtype == kF16 ? up_launch<kF16>(a, c.wide, up, s) : up_launch<kBF16>(a, c.wide, up, s);
+    return set.dtype == kF16 ? up_launch<kF16>(a, c.many, up, s) : up_launch<kBF16>(a, c.many, up, s);
 }
 
 }  // namespace q4gsw

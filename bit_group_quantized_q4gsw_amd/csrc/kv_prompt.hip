@@ -104,7 +104,7 @@ __global__ __launch_bounds__(64 * NW, (D <= 128 ? 2 : 1)) void kv_prompt_kernel(
     const int tok0 = r0 / a.group;
     const KvTree tree(lds + 2 * kStage, a.max_new);
     if constexpr (TREE) {
-        KvTree(tree).build(a.parents, s.first_row, min(s.m, a.max_new), tok0,
+        tree.build(a.parents, s.first_row, min(s.m, a.max_new), tok0,
                            (min(r0 + 32 * NW, rows) - 1) / a.group + 1 - tok0, a.window);
         if (ok) place = p0 + tree.depth(tok - tok0);     // its position
     }

@@ -132,7 +132,7 @@ __global__ __launch_bounds__(512, kv_rows_waves(D)) void kv_rows_kernel(KvAttnAr
     const int tok0 = r0 / a.group, p0 = s.len - s.m;
     const KvTree tree(reinterpret_cast<uint8_t*>(smem) + a.tree_at, a.max_new);
     if constexpr (TREE) {
-        KvTree(tree).build(a.parents, s.first_row, min(s.m, a.max_new), tok0, (r0 + nr - 1) / a.group + 1 - tok0, a.window);
+        tree.build(a.parents, s.first_row, min(s.m, a.max_new), tok0, (r0 + nr - 1) / a.group + 1 - tok0, a.window);
         if (ok) place = p0 + tree.depth(tok - tok0);          // its position
     }
 

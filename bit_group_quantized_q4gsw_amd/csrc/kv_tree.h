@@ -32,7 +32,7 @@ __host__ __device__ inline int tree_bytes(int nodes, int tokens) {
 __device__ __forceinline__ int16_t tree_parent(int raw, int node) { return (int16_t)(raw >= 0 && raw < node ? raw : -1); }
 
 struct KvTree {
-    const int16_t* up;
+    int16_t* up;
     uint32_t* bits;                      // [token - first][stride]
     int stride, words;
 
@@ -63,11 +63,13 @@ struct KvTree {
         }
         row[words + 2] = (uint32_t)depth;
     }
+    // The parent of `node` as the caller gave it.
+    __device__ __forceinline__ void put(int node, int raw) const { up[node] = tree_parent(raw, node); }
     // All threads of the workgroup: the parents of the first `nodes` nodes of the sequence at token row
     // `first_row`, then the sets of tokens [tok0, tok0 + tokens).
-    __device__ __forceinline__ void build(const int32_t* parents, int64_t first_row, int nodes, int tok0, int tokens, int window) {
+    __device__ __forceinline__ void build(const int32_t* parents, int64_t first_row, int nodes, int tok0, int tokens, int window) const {
         for (int j = threadIdx.x; j < nodes; j += blockDim.x)
-            const_cast<int16_t*>(up)[j] = tree_parent(parents[first_row + j], j);
+            put(j, parents[first_row + j]);
         __syncthreads();
         for (int t = threadIdx.x; t < tokens; t += blockDim.x) climb(tok0 + t, window, bits + t * stride);
         __syncthreads();

@@ -470,7 +470,7 @@ q4gsw_status q4gsw_logits_adjust(const void* logits, int32_t dtype, int64_t rows
     if (!act_dtype_ok(dtype)) return Q4GSW_E_DTYPE;
     if (r->batch < 1 || r->batch > (1 << 20)) return rows == 0 && r->batch == 0 ? Q4GSW_OK : Q4GSW_E_SHAPE;
     if (!r->cu && r->batch != rows) return Q4GSW_E_SHAPE;
-    if (r->max_new < 1 || r->max_new > (r->parents ? kTreeMax : kMaxM)) return Q4GSW_E_SHAPE;
+    if (r->max_new < 1 || r->max_new > (r->cu && r->ids ? kTreeMax : kMaxM)) return Q4GSW_E_SHAPE;
     if (r->parents && (!r->cu || !r->ids)) return Q4GSW_E_NULL;
     if (r->history && (r->history_cols < 0 || r->history_ld < r->history_cols || r->history_ld > kMaxDim)) return Q4GSW_E_SHAPE;
     if (r->history && !r->history_len) return Q4GSW_E_NULL;
@@ -483,6 +483,7 @@ q4gsw_status q4gsw_logits_adjust(const void* logits, int32_t dtype, int64_t rows
                  r->history_len, r->prompt_len, r->ids, r->parents, r->repetition, r->presence, r->frequency, r->bias_ids,
                  r->bias, r->bias_ld, r->bias_cols, r->mask, r->mask_ld, 0, 0, false};
     if (!r->history) a.prompt_len = nullptr;
+    if (!r->cu) a.max_new = 1;
     if (!logits_launch_ok(a)) return Q4GSW_E_SHAPE;
     const int es = esize(dtype);
     const uint64_t B = (uint64_t)r->batch;

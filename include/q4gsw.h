@@ -621,9 +621,10 @@ q4gsw_status q4gsw_kv_keep(const q4gsw_kv_cache *caches, int32_t count, const q4
  *                int32 [batch]; at most history_cols) entries of row b are the tokens sequence b has behind it,
  *                of which the first prompt_len[b] (device int32 [batch]; NULL: none) are seen but not generated
  *   ids          device int32 [rows], or NULL: the tokens of the rows themselves.  A row has seen and
- *                generated its own token and those of the rows of its sequence before it, or with
- *   parents      (device int32 [rows], as in q4gsw_kv_tree_attention; needs cu, ids and max_new at most 512)
- *                those of its ancestors only
+ *                generated its own token and those of the rows of its sequence before it (with cu: max_new at
+ *                most 512), or with
+ *   parents      (device int32 [rows], as in q4gsw_kv_tree_attention; needs cu and ids) those of its
+ *                ancestors only
  *   repetition, presence, frequency   device fp32 [batch], or NULL: 1, 0 and 0
  *   bias_ids     device int32 [batch][bias_ld >= bias_cols], or NULL, with bias, device fp32 of the same shape:
  *                of entries with one token the last counts
