@@ -166,6 +166,11 @@ struct QueryRow {
 // for 64 .. 256 channels: sums D / 4, queries D / 8).
 constexpr int kv_rows_waves(int D) { return D == 64 ? 4 : (D <= 128 ? 3 : 2); }
 
+// The same of the kernel of trees: 109, 142, 167, 223 and some 280 for 64 .. 256 channels, 17 to 21 more with
+// `prec` (sums D / 2, queries D / 4).  At 256 channels a workgroup has at most four waves.
+constexpr int kv_tree_waves(int D, bool prec) { return D == 64 ? 4 : (D == 96 || (D == 128 && !prec) ? 3 : (D <= 192 ? 2 : 1)); }
+constexpr int kv_tree_most(int D) { return D == 256 ? 4 : 8; }      // waves of a workgroup
+
 // The kernel of many rows: blocks of 32 tokens in a tile (two, but one where two with the remainders
 // that `prec` keeps do not fit LDS twice), bytes of its two stages of keys and values, and how many of
 // its workgroups of `waves` a CU of 160 KB holds: registers allow two waves a SIMD up to 128 channels and one
@@ -184,6 +189,8 @@ inline int tree_lds(const KvAttnArgs& a, int rows) {
 
 // kv_rows.hip: `waves` (4 or 8) per workgroup, tiles of 16 rows.
 hipError_t launch_kv_rows(const KvAttnArgs& a, int waves, hipStream_t s);
+// kv_tree.hip: `waves` (4, or 8 up to 192 channels) per workgroup, tiles of 32 rows.
+hipError_t launch_kv_tree(const KvAttnArgs& a, int waves, hipStream_t s);
 // kv_prompt.hip: 32 rows a wave, `waves` 4, or 8 up to 128 channels; a.chunk even.
 hipError_t launch_kv_prompt(const KvAttnArgs& a, int waves, hipStream_t s);
 // The join of the splits' partials into out.

@@ -74,7 +74,7 @@ uint64_t rows_extent(int64_t tokens, int64_t ld, int64_t row, int es) {
 
 // How an attention call runs.
 struct AttnPlan {
-    bool prompt;                 // kv_prompt, else kv_rows
+    enum { kRows, kTree, kPrompt } kernel;
     int waves;                   // per workgroup
     int row_tiles, splits, chunk;
     float us;                    // estimate
@@ -138,6 +138,30 @@ AttnPlan plan_rows(const AttnSize& n) {
     return p;
 }
 
+// us that a CU takes for a unit of 32 keys and 32 rows of a tree (one wave a SIMD at 256 channels).
+float tree_unit(int dim, bool prec) {
+    return (dim <= 192 ? 0.04f + 0.0017f * dim : 0.6f) * (prec ? 1.25f : 1.0f);
+}
+
+// Trees of more than 16 rows, tiles of 32.  VALU is the bound, so one workgroup of eight waves a CU (four at 256 channels) does as
+// well as more, and splits pay while they fill the CUs: us of 16 sequences of 1024 .. 4096 tokens, 32 / 8 heads of
+// 128, bf16 (fp16), 8 nodes (128 workgroups): 1 split 38 (47), 2 splits 27 (32), 4 splits 28 (32), 8 splits 33 (40);
+// 16 nodes (256): 39 (47), 42 (51), 46 (56), 51 (65); 64 nodes (1024): 88 (117), 98 (128); 17 blocks, heads of 64: 1
+// split 9.7, 2 splits 11.9.
+AttnPlan plan_tree(const AttnSize& n) {
+    AttnPlan p{};
+    p.kernel = AttnPlan::kTree;
+    p.row_tiles = (n.rows + 31) / 32;
+    const int64_t groups = (int64_t)n.batch * n.heads * p.row_tiles, blocks = n.blocks(32);
+    int64_t splits = 1;
+    if (blocks > 32) splits = kCus / groups < blocks / 8 ? kCus / groups : blocks / 8;
+    finish_plan(p, n, blocks, splits);
+    p.waves = groups * p.splits <= kCus && kv_tree_most(n.dim) == 8 ? 8 : 4;
+    const float all = groups * n.mean / kCus, longest = (float)((p.chunk + p.waves - 1) / p.waves * p.waves);
+    p.us += 4.5f + 0.035f * n.dim + tree_unit(n.dim, n.prec) * (longest > all ? longest : all);
+    return p;
+}
+
 // us of a turn of 64 keys of a workgroup that fills its CU (eight waves up to 128 channels, four above).
 float prompt_turn(int dim, bool prec) {
     if (dim <= 128) return prec ? 0.66f + 0.0235f * dim : 0.65f + 0.0135f * dim;
@@ -166,7 +190,7 @@ AttnPlan plan_prompt(const AttnSize& n) {
     AttnPlan best{};
     for (int waves = n.dim <= 128 ? 8 : 4; waves >= 4; waves -= 4) {
         AttnPlan p{};
-        p.prompt = true;
+        p.kernel = AttnPlan::kPrompt;
         p.waves = waves;
         p.row_tiles = (n.rows + 32 * waves - 1) / (32 * waves);
         const int64_t groups = (int64_t)n.batch * n.heads * p.row_tiles, most = prompt_splits(n, waves, n.prec);
@@ -204,7 +228,13 @@ AttnSize attention_size(int heads, int dim, int batch, int hq, int max_new, int 
 // them windowed, it takes the slower kernel by over 10% for 12, by 31% at most.  Up to 32 rows never fill the workgroup of many.
 AttnPlan plan_attention(const AttnSize& n, int kernel) {
     if (kernel == Q4GSW_KV_MANY_ROWS) return plan_prompt(n);
-    const AttnPlan few = plan_rows(n);
+    AttnPlan few = plan_rows(n);
+    // a tree's tiles of 32 rows cost a unit less VALU, tiles of 16 spread over more CUs and start sooner (16 nodes of 600
+    // tokens, 32 / 8 heads of 128, bf16: 11.9 us against 14.2; the batch of plan_tree's comment, 8 nodes: 33 against 28)
+    if (n.tree && n.rows > 16) {
+        const AttnPlan wide = plan_tree(n);
+        if (wide.us < few.us) few = wide;
+    }
     if (n.rows <= kFewRows || kernel == Q4GSW_KV_FEW_ROWS) return few;
     const AttnPlan many = plan_prompt(n);
     return many.us < few.us ? many : few;
@@ -286,7 +316,8 @@ q4gsw_status attend(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s, const int32
     a.row_tiles = p.row_tiles;
     a.parents = tree ? parents : nullptr;
     hipStream_t st_ = static_cast<hipStream_t>(stream);
-    hipError_t e = p.prompt ? launch_kv_prompt(a, p.waves, st_) : launch_kv_rows(a, p.waves, st_);
+    hipError_t e = p.kernel == AttnPlan::kPrompt ? launch_kv_prompt(a, p.waves, st_)
+                   : p.kernel == AttnPlan::kTree ? launch_kv_tree(a, p.waves, st_) : launch_kv_rows(a, p.waves, st_);
     if (e == hipSuccess && p.splits > 1) e = launch_kv_join(a, st_);
     return hip_status(e);
 }
@@ -393,7 +424,7 @@ q4gsw_status q4gsw_kv_attention_plan(const q4gsw_kv_cache* c, int32_t batch, int
     int kernel = 0;
     if ((st = read_kernel(opts, c, hq, max_new, &kernel)) != Q4GSW_OK) return st;
     const AttnPlan p = plan_attention(attention_size(c->heads, c->dim, batch, hq, max_new, max_ctx, window, dtype), kernel);
-    *info = q4gsw_kv_plan_info{p.prompt ? Q4GSW_KV_MANY_ROWS : Q4GSW_KV_FEW_ROWS, p.waves, p.splits};
+    *info = q4gsw_kv_plan_info{p.kernel == AttnPlan::kPrompt ? Q4GSW_KV_MANY_ROWS : Q4GSW_KV_FEW_ROWS, p.waves, p.splits};
     return Q4GSW_OK;
 }
 
