@@ -105,7 +105,7 @@ class KvOptions(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-KV_KERNELS = {"any": 0, "few_rows": 1, "many_rows": 2}
+KV_KERNELS = {"any": 0, "few_rows": 1, "many_rows": 2, "tree": 3}
 
 
 # Choices made by forced_route / forced_plan, held per Python thread and handed to each call
@@ -1089,7 +1089,7 @@ def forced_route(name: str):
 @contextlib.contextmanager
 def forced_kv_kernel(name: str):
     """Send the kv_attention calls made by this thread inside the block to one kernel, "few_rows" or
-    "many_rows" (tests and benchmarks); Q4gswError with E_ROUTE where it cannot serve a call."""
+    "many_rows", or the kv_tree_attention calls to either or to "tree" (tests and benchmarks); Q4gswError with E_ROUTE where it cannot serve a call."""
     old = _local.kv
     _local.kv = ctypes.pointer(KvOptions(KV_KERNELS[name], 0))
     try:

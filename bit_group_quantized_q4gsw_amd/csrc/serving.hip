@@ -228,14 +228,16 @@ AttnSize attention_size(int heads, int dim, int batch, int hq, int max_new, int 
 // them windowed, it takes the slower kernel by over 10% for 12, by 31% at most.  Up to 32 rows never fill the workgroup of many.
 AttnPlan plan_attention(const AttnSize& n, int kernel) {
     if (kernel == Q4GSW_KV_MANY_ROWS) return plan_prompt(n);
+    if (kernel == Q4GSW_KV_TREE) return plan_tree(n);
     AttnPlan few = plan_rows(n);
+    if (kernel == Q4GSW_KV_FEW_ROWS) return few;
     // a tree's tiles of 32 rows cost a unit less VALU, tiles of 16 spread over more CUs and start sooner (16 nodes of 600
     // tokens, 32 / 8 heads of 128, bf16: 11.9 us against 14.2; the batch of plan_tree's comment, 8 nodes: 33 against 28)
     if (n.tree && n.rows > 16) {
         const AttnPlan wide = plan_tree(n);
         if (wide.us < few.us) few = wide;
     }
-    if (n.rows <= kFewRows || kernel == Q4GSW_KV_FEW_ROWS) return few;
+    if (n.rows <= kFewRows) return few;
     const AttnPlan many = plan_prompt(n);
     return many.us < few.us ? many : few;
 }
@@ -253,11 +255,11 @@ q4gsw_status check_attention(const q4gsw_kv_cache* c, int64_t batch, int64_t tok
     return Q4GSW_OK;
 }
 
-q4gsw_status read_kernel(const q4gsw_kv_options* o, const q4gsw_kv_cache* c, int32_t hq, int32_t max_new, int* kernel) {
+q4gsw_status read_kernel(const q4gsw_kv_options* o, const q4gsw_kv_cache* c, int32_t hq, int32_t max_new, bool tree, int* kernel) {
     *kernel = o ? o->kernel : Q4GSW_KV_ANY;
     if (!o) return Q4GSW_OK;
     if (o->reserved != 0) return Q4GSW_E_SHAPE;
-    if (*kernel < Q4GSW_KV_ANY || *kernel > Q4GSW_KV_MANY_ROWS) return Q4GSW_E_ROUTE;
+    if (*kernel < Q4GSW_KV_ANY || *kernel > (tree ? Q4GSW_KV_TREE : Q4GSW_KV_MANY_ROWS)) return Q4GSW_E_ROUTE;
     if (*kernel == Q4GSW_KV_MANY_ROWS && (int64_t)max_new * (hq / c->heads) <= kFewRows) return Q4GSW_E_ROUTE;
     return Q4GSW_OK;
 }
@@ -276,7 +278,7 @@ q4gsw_status attend(const q4gsw_kv_cache* c, const q4gsw_kv_seqs* s, const int32
     if (window < 0 || !(softcap == 0.0f || (softcap >= kMinCap && softcap <= kMaxCap))) return Q4GSW_E_SHAPE;
     if (!act_dtype_ok(dtype)) return Q4GSW_E_DTYPE;
     int kernel = 0;
-    if ((st = read_kernel(opts, c, hq, max_new, &kernel)) != Q4GSW_OK) return st;
+    if ((st = read_kernel(opts, c, hq, max_new, tree, &kernel)) != Q4GSW_OK) return st;
     if (s->tokens == 0) return Q4GSW_OK;
     if (!q || !out || (tree && !parents)) return Q4GSW_E_NULL;
     const int64_t row = (int64_t)hq * c->dim;
@@ -422,7 +424,7 @@ q4gsw_status q4gsw_kv_attention_plan(const q4gsw_kv_cache* c, int32_t batch, int
     if (window < 0) return Q4GSW_E_SHAPE;
     if (!act_dtype_ok(dtype)) return Q4GSW_E_DTYPE;
     int kernel = 0;
-    if ((st = read_kernel(opts, c, hq, max_new, &kernel)) != Q4GSW_OK) return st;
+    if ((st = read_kernel(opts, c, hq, max_new, false, &kernel)) != Q4GSW_OK) return st;
     const AttnPlan p = plan_attention(attention_size(c->heads, c->dim, batch, hq, max_new, max_ctx, window, dtype), kernel);
     *info = q4gsw_kv_plan_info{p.kernel == AttnPlan::kPrompt ? Q4GSW_KV_MANY_ROWS : Q4GSW_KV_FEW_ROWS, p.waves, p.splits};
     return Q4GSW_OK;

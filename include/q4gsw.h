@@ -543,7 +543,8 @@ q4gsw_status q4gsw_kv_attention(const q4gsw_kv_cache *c, const q4gsw_kv_seqs *s,
 typedef enum q4gsw_kv_kernel {
     Q4GSW_KV_ANY = 0,
     Q4GSW_KV_FEW_ROWS = 1,    /* a wave per 32-token unit, tiles of 16 rows */
-    Q4GSW_KV_MANY_ROWS = 2    /* 32 rows a wave, tiles of keys shared by the workgroup */
+    Q4GSW_KV_MANY_ROWS = 2,   /* 32 rows a wave, tiles of keys shared by the workgroup */
+    Q4GSW_KV_TREE = 3         /* q4gsw_kv_tree_attention only: a wave per 32-token unit, tiles of 32 rows */
 } q4gsw_kv_kernel;
 typedef struct q4gsw_kv_options {
     int32_t kernel;           /* q4gsw_kv_kernel */

@@ -9,7 +9,9 @@ import pytest
 import torch
 
 from tests.gpu_helpers import lib
+from tests.serving_model import kv_values
 from tests.test_gpu_kv_attention import BF16, F16, F32, check, fill, offsets
+from tests.test_gpu_kv_cache import build
 from tests.tree_model import forest, tree_attention
 
 pytestmark = pytest.mark.gpu
@@ -68,15 +70,15 @@ def test_against_the_formula(nodes, lens, kind, hq, hkv, dim, page, dtype, windo
 
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
-@pytest.mark.parametrize("kernel", ["few_rows", "many_rows"])
-def test_both_kernels(kernel, dim, dtype):
+@pytest.mark.parametrize("kernel", ["few_rows", "tree", "many_rows"])
+def test_every_kernel(kernel, dim, dtype):
     """Every instance, at places where a tree begins and ends inside a block, with and without a window."""
     q = lib()
     for lens, window in (([70, 97, 33], 0), ([66, 95, 40], 9)):
         run(q, [forest(n, "far", n) for n in (37, 21, 33)], lens, 4, 2, dim, 32, dtype, window, seed=dim, kernel=kernel)
 
 
-@pytest.mark.parametrize("kernel", ["few_rows", "many_rows"])
+@pytest.mark.parametrize("kernel", ["few_rows", "tree", "many_rows"])
 @pytest.mark.parametrize("group", [1, 3, 8, 40])
 @pytest.mark.parametrize("start", [0, 1, 31, 32, 63])
 def test_places_of_the_tree(start, group, kernel):
@@ -115,25 +117,53 @@ def test_rows_without_keys_and_hidden_pages():
     where = (table, offsets([20, 30]), ln, 30, 70)
     paged = [torch.tensor([32 <= t < 64 for t in range(70)]), torch.ones(20, dtype=torch.bool)]
     want, bound = tree_attention(x, keys, values, trees, lens, paged=paged)
-    for kernel in ("few_rows", "many_rows"):
+    for kernel in ("few_rows", "tree", "many_rows"):
         with q.forced_kv_kernel(kernel):
             got = q.kv_tree_attention(cache, x.cuda(), ints(trees[0] + trees[1]), *where)
         check(got, want, bound, f"hidden {kernel}")
         assert (got[20:30] == 0).all()                                            # places -10 .. -1
 
 
-def test_a_split_cache():
+@pytest.mark.parametrize("kernel", ["few_rows", "tree", "many_rows"])
+@pytest.mark.parametrize("dim,dtype,window", [(128, F16, 0), (64, BF16, 0), (256, F32, 0), (96, BF16, 7000)])
+def test_a_split_cache(kernel, dim, dtype, window):
     """Long caches of few rows split the keys; the join and a poisoned workspace."""
     q = lib()
     trees, lens = [forest(9, "near", 1), forest(5, "far", 2)], [9000, 300]
-    cache, table, ln, keys, values = fill(q, lens, 1, 128, 64, F16, 5)
-    x = torch.randn(14, 8, 128, generator=torch.Generator().manual_seed(2)).half()
+    cache, table, ln, keys, values = fill(q, lens, 1, dim, 64, dtype, 5)
+    x = torch.randn(14, 8, dim, generator=torch.Generator().manual_seed(2)).to(dtype)
     need = q.kv_tree_attention_workspace_bytes(cache, 2, 14, 8, 9, 9000)
     assert need > 0
     ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
-    got = q.kv_tree_attention(cache, x.cuda(), ints(trees[0] + trees[1]), table, offsets([9, 5]), ln, 9, 9000, workspace=ws)
-    want, bound = tree_attention(x, keys, values, trees, lens)
-    check(got, want, bound, "split")
+    with q.forced_kv_kernel(kernel):
+        got = q.kv_tree_attention(cache, x.cuda(), ints(trees[0] + trees[1]), table, offsets([9, 5]), ln, 9, 9000, window=window,
+                                  workspace=ws)
+    want, bound = tree_attention(x, keys, values, trees, lens, window)
+    check(got, want, bound, f"split {kernel} {dim}")
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_scales_that_rise_and_fall(dim, dtype):
+    """Values whose scales differ by 2^30 along the cache, in either order, and scores that climb far: the running
+    references move, and what was summed before stays in range."""
+    q = lib()
+    n, m = 200, 24
+    cache, table, cu, ln, k, v = build(q, [n], [n], 1, dim, 64, torch.float32, 3)
+    for order in (1, -1):
+        size = torch.logspace(-6, 3, n)[:, None, None]
+        size = size if order == 1 else size.flip(0)
+        kk, vv = k * (0.2 + 0.02 * torch.arange(n))[:, None, None], v * size
+        q.kv_append(cache, kk.cuda(), vv.cuda(), table, cu, ln)
+        x = torch.randn(m, 4, dim, generator=torch.Generator().manual_seed(2)).to(dtype)
+        tree = forest(m, "near", 3)
+        want, bound = tree_attention(x, [kv_values(kk)], [kv_values(vv)], [tree], [n])
+        for kernel in ("few_rows", "tree", "many_rows"):
+            with q.forced_kv_kernel(kernel):
+                got = q.kv_tree_attention(cache, x.cuda(), ints(tree), table, offsets([m]), ln, m, n).cpu().double()
+            # the roundings of weights are relative to their products with scales: of the largest in the row's sum
+            assert torch.isfinite(got).all()
+            assert float(((got - want).abs() / bound).max()) <= 1, (kernel, order)
 
 
 def test_queries_that_are_not_finite():

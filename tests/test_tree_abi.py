@@ -1,6 +1,7 @@
 """Refusals of the calls for trees of drafted tokens, on the host: every call here fails validation before
 any HIP call, so made-up device addresses are safe."""
 import ctypes
+import itertools
 
 import pytest
 import torch
@@ -51,6 +52,8 @@ def test_tree_attention_refusals(q):  # noqa: F811
     s = seqs(q)
     assert lib.q4gsw_kv_tree_attention_ex(r(c), r(s), UP, X, 1024, q.F16, 8, 2, 9, 0, 0.0, OUT, WS, need, r(opts), None) == 11
     # no kernel of many rows up to 32 rows
+    opts.kernel = 4
+    assert lib.q4gsw_kv_tree_attention_ex(r(c), r(s), UP, X, 1024, q.F16, 8, 2, 9, 0, 0.0, OUT, WS, need, r(opts), None) == 11
     opts.kernel = 2
     assert lib.q4gsw_kv_tree_attention_ex(r(c), r(s), UP, X, 1024, q.F16, 8, 2, 9, 0, 0.0, OUT, WS, need, r(opts), None) == 11
 
@@ -58,16 +61,19 @@ def test_tree_attention_refusals(q):  # noqa: F811
 def test_a_window_never_needs_more_workspace(q):  # noqa: F811
     lib, r = q.lib(), ctypes.byref
     n = ctypes.c_uint64()
-    c = cache(q, heads=1)
-    for new in (1, 16, 64, 300, 512):
-        for ctx in (600, 5000, 131072):
-            for batch in (1, 7, 100):
-                s = seqs(q, batch=batch, tokens=new * batch)
-                assert lib.q4gsw_kv_tree_attention_workspace_bytes(r(c), batch, new * batch, 4, new, ctx, r(n)) == S_OK
-                for win in (1, 33, 500, 4096, 100000):
-                    st = lib.q4gsw_kv_tree_attention(r(c), r(s), FAKE * 200, X, 512, q.F16, 4, new, ctx, win, 0.0, X, FAKE * 100,
-                                                     n.value, None)
-                    assert st == E_ALIAS, (new, ctx, batch, win, st)
+    opts = q.binding.KvOptions(0, 0)
+    for heads, dim, new, kernel in itertools.product((1, 3), (64, 128, 256), (1, 5, 16, 64, 300, 512), (0, 1, 2, 3)):
+        if kernel == 2 and 4 * new <= 32:
+            continue
+        c = cache(q, heads=heads, dim=dim)
+        opts.kernel = kernel
+        for ctx, batch in itertools.product((600, 5000, 131072), (1, 7, 100)):
+            s = seqs(q, batch=batch, tokens=new * batch)
+            assert lib.q4gsw_kv_tree_attention_workspace_bytes(r(c), batch, new * batch, 4 * heads, new, ctx, r(n)) == S_OK
+            for win, dt in itertools.product((0, 1, 500, 4096, 100000), (q.F16, q.BF16)):
+                st = lib.q4gsw_kv_tree_attention_ex(r(c), r(s), FAKE * 200, X, 4 * heads * dim, dt, 4 * heads, new, ctx, win, 0.0, X,
+                                                    FAKE * 100, n.value, r(opts), None)
+                assert st == E_ALIAS, (heads, dim, kernel, new, ctx, batch, win, st)
 
 
 def caches(q, *each):  # noqa: F811
