@@ -11,8 +11,13 @@
 //   * out = y + alpha t B_s^T: factors as the first operand of the 16x16x16 product, so that a lane ends
 //     with eight neighbouring columns of one row.  With few rows the waves of a workgroup share the adapters of
 //     16 rows (a row is its adapter's wave's alone), with many they share the columns.
+// Few rows of small factors take one launch, in which every workgroup of the second computes t itself.
 // Rows need no order: adapters are found among each 16 rows by comparison, and one that many tiles share
 // is read from L2 by all but the first.
+//
+// Bound: bytes of the factors and latency: 61 rows of 48 adapters, rank 32, K = 8192, N = 2048, fp32 rows, fp16 factors:
+// 12 us (29 MB through L2, 18 from HBM) + 5 us; 64 rows of 32 adapters, rank 16, K = 2048, N = 8192: 6.4 + 7 us.  Prompts: the
+// second launch's y, read and written: 2048 rows of 8192: 7.5 + 33 us for 134 MB.
 //
 // Numbers: products of 16-bit factors are exact in the matrix unit's fp32, so what rows and t lose on
 // their way into 16-bit operands is all that is lost.  They enter as sums of parts: with bf16 factors one
@@ -111,12 +116,68 @@ struct Octet {
 constexpr int kWaves = 8;                // of a workgroup, which share a chunk of K
 constexpr int kMostChunks = 4;
 
+// Steps [s0, s1) of 32 columns of t for 16 rows and 16 ranks: lane (i, q) gets ranks 4 q .. + 3 of row i, where
+// `match`.  A: the adapter's runs of these ranks, `stride` bytes a step, at this lane.
+template <int FT, int XT, bool VEC>
+__device__ __forceinline__ f4 down_part(const AdapterArgs& a, const uint8_t* A, int64_t stride, int64_t row, bool match, int q,
+                                        int64_t s0, int64_t s1) {
+    constexpr int P = row_parts<FT, XT>();
+    constexpr bool SCALED = FT == kF16 && XT != kF16;
+    constexpr int kSteps = 8;                             // loaded together
+    f4 sum = {0.f, 0.f, 0.f, 0.f};
+    for (; s0 < s1; s0 += kSteps) {
+        u4 av[kSteps];
+        Octet<XT, VEC> xv[kSteps];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            av[s] = u4{0u, 0u, 0u, 0u};
+            xv[s].clear();
+            if (s0 + s < s1) av[s] = ldg16(A + (s0 + s) * stride);
+        }
+        if (match) {
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                if (s0 + s < s1) xv[s].load(a.x, row, 32 * (s0 + s) + 8 * q, a.K);
+        }
+        float mul = 1.0f, inv = 1.0f;
+        if constexpr (SCALED) {
+            float amax = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(xv[s][e]));
+            row_factor(wave_max_rows(amax), mul, inv);
+        }
+        f4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            if constexpr (FT == XT) {
+                acc = mfma32<FT>(av[s], xv[s].w[0], acc);
+            } else {
+                u4 part[P];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v0 = xv[s][2 * e], v1 = xv[s][2 * e + 1];
+                    if constexpr (SCALED) {
+                        v0 *= mul;
+                        v1 *= mul;
+                    }
+#pragma unroll
+                    for (int p = 0; p < P; ++p) part[p][e] = take_part<FT>(v0, v1);
+                }
+#pragma unroll
+                for (int p = 0; p < P; ++p) acc = mfma32<FT>(av[s], part[p], acc);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = SCALED ? fmaf(acc[e], inv, sum[e]) : sum[e] + acc[e];
+    }
+    return sum;
+}
+
 // t of 16 rows, 16 ranks and a chunk of K: t[chunk][m][rank].
 template <int FT, int XT, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void down_kernel(AdapterArgs a) {
-    constexpr int P = row_parts<FT, XT>();
-    constexpr bool SCALED = FT == kF16 && XT != kF16;
-    constexpr int kSteps = 8;                             // of 32 columns, loaded together
     __shared__ f4 s_sum[kWaves][64];
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -137,56 +198,7 @@ __global__ __launch_bounds__(64 * kWaves) void down_kernel(AdapterArgs a) {
         const int slot = __builtin_amdgcn_readlane(mine, __builtin_ctz(firsts));
         const bool match = mine == slot;
         const uint8_t* A = a.set.data + slot * a.set.slot_bytes + 1024 * (int64_t)rt + 16 * lane;
-        f4 sum = {0.f, 0.f, 0.f, 0.f};
-        for (int64_t s0 = begin; s0 < s1; s0 += kSteps) {
-            u4 av[kSteps];
-            Octet<XT, VEC> xv[kSteps];
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                av[s] = u4{0u, 0u, 0u, 0u};
-                xv[s].clear();
-                if (s0 + s < s1) av[s] = ldg16(A + (s0 + s) * a.rank_tiles * 1024);
-            }
-            if (match) {
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-                    if (s0 + s < s1) xv[s].load(a.x, row, 32 * (s0 + s) + 8 * q, a.K);
-            }
-            float mul = 1.0f, inv = 1.0f;
-            if constexpr (SCALED) {
-                float amax = 0.0f;
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(xv[s][e]));
-                row_factor(wave_max_rows(amax), mul, inv);
-            }
-            f4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                if constexpr (FT == XT) {
-                    acc = mfma32<FT>(av[s], xv[s].w[0], acc);
-                } else {
-                    u4 part[P];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v0 = xv[s][2 * e], v1 = xv[s][2 * e + 1];
-                        if constexpr (SCALED) {
-                            v0 *= mul;
-                            v1 *= mul;
-                        }
-#pragma unroll
-                        for (int p = 0; p < P; ++p) part[p][e] = take_part<FT>(v0, v1);
-                    }
-#pragma unroll
-                    for (int p = 0; p < P; ++p) acc = mfma32<FT>(av[s], part[p], acc);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum[e] = SCALED ? fmaf(acc[e], inv, sum[e]) : sum[e] + acc[e];
-        }
-        // lane (i, q) holds ranks 4 q .. + 3 of row i
-        s_sum[wave][lane] = sum;
+        s_sum[wave][lane] = down_part<FT, XT, VEC>(a, A, 1024 * (int64_t)a.rank_tiles, row, match, q, begin, s1);
         __syncthreads();
         if (tid < 256) {
             const int l = tid >> 2, e = tid & 3, ri = l & 15;
@@ -199,10 +211,14 @@ __global__ __launch_bounds__(64 * kWaves) void down_kernel(AdapterArgs a) {
     }
 }
 
-// out = y + alpha t B^T for 16 rows, S steps of 16 ranks.  MANY: 256 columns, 64 a wave; else 32 J columns,
-// every fourth adapter of the rows a wave.
-template <int FT, int S, bool MANY>
-__global__ __launch_bounds__(256) void up_kernel(AdapterArgs a) {
+// out = y + alpha t B^T for 16 rows, S steps of 16 ranks.  kMany: 256 columns, 64 a wave.  kFew: 32 J columns,
+// the adapters of the rows dealt to the waves.  kOne: as kFew, of one tile of rows, and t is computed here, by every
+// workgroup once more (XT: the rows' type, which the others do not look at).
+enum UpKind { kFew, kMany, kOne };
+template <int FT, int S, UpKind KIND, int XT>
+__global__ __launch_bounds__(KIND == kOne ? 64 * kWaves : 256) void up_kernel(AdapterArgs a) {
+    constexpr bool MANY = KIND == kMany;
+    constexpr int NW = KIND == kOne ? kWaves : 4;
     constexpr int J = MANY || S == 1 ? 2 : 1;             // blocks of 32 columns a wave
     constexpr int kBatch = MANY ? 1 : 4;                  // adapters whose factors are loaded together
     constexpr int P = FT == kF16 ? 2 : 3;
@@ -220,11 +236,11 @@ __global__ __launch_bounds__(256) void up_kernel(AdapterArgs a) {
         firsts = 0;
         here = here && mine < 0 && wave == 0;
         for (int n = 0; left; left &= left - 1, ++n) {
-            if ((n & 3) != wave) continue;
+            if (n % NW != wave) continue;
             firsts |= left & (0u - left);
             here |= mine == __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
         }
-        if (!__any(here)) return;
+        if (KIND != kOne && !__any(here)) return;
     }
 
     // t and what the columns hold so far
@@ -232,7 +248,32 @@ __global__ __launch_bounds__(256) void up_kernel(AdapterArgs a) {
     float alpha = 0.0f;
 #pragma unroll
     for (int s = 0; s < S; ++s) tv[s] = f4{0.f, 0.f, 0.f, 0.f};
-    if (here && mine >= 0) {
+    if constexpr (KIND == kOne) {
+        __shared__ f4 s_t[kWaves][S][64];
+        const int64_t steps = a.set.k_pad >> 5, per = (steps + kWaves - 1) / kWaves;
+        for (uint32_t left = first_rows(mine, i); left; left &= left - 1) {
+            const int slot = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
+            const bool match = mine == slot;
+            const uint8_t* A = a.set.data + slot * a.set.slot_bytes + 16 * lane;
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                s_t[wave][s][lane] = down_part<FT, XT, true>(a, A + 1024 * s, 1024 * S, m * a.K, match, q, per * wave, min(per * (wave + 1), steps));
+            __syncthreads();
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                f4 t = s_t[0][s][lane];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) t[e] += s_t[w][s][lane][e];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tv[s][e] = match ? t[e] : tv[s][e];
+            }
+            __syncthreads();
+        }
+        if (mine >= 0) alpha = a.set.alpha[mine];
+        if (!__any(here)) return;
+    } else if (here && mine >= 0) {
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const float* t = a.t + m * (16 * S) + 16 * s + 4 * q;
@@ -389,8 +430,8 @@ template <int FT>
 hipError_t up_launch(const AdapterArgs& a, bool many, dim3 grid, hipStream_t s) {
 #define Q4GSW_UP(S)                                                                                   \
     case S:                                                                                           \
-        if (many) hipLaunchKernelGGL((up_kernel<FT, S, true>), grid, dim3(256), 0, s, a);             \
-        else hipLaunchKernelGGL((up_kernel<FT, S, false>), grid, dim3(256), 0, s, a);                 \
+        if (many) hipLaunchKernelGGL((up_kernel<FT, S, kMany, kF32>), grid, dim3(256), 0, s, a);      \
+        else hipLaunchKernelGGL((up_kernel<FT, S, kFew, kF32>), grid, dim3(256), 0, s, a);            \
         break;
     switch (a.rank_tiles) {
         Q4GSW_UP(1)
@@ -400,6 +441,13 @@ hipError_t up_launch(const AdapterArgs& a, bool many, dim3 grid, hipStream_t s) 
         default: return hipErrorInvalidValue;
     }
 #undef Q4GSW_UP
+    return hipGetLastError();
+}
+
+template <int FT, int XT>
+hipError_t one_launch(const AdapterArgs& a, dim3 grid, hipStream_t s) {
+    if (a.rank_tiles == 1) hipLaunchKernelGGL((up_kernel<FT, 1, kOne, XT>), grid, dim3(64 * kWaves), 0, s, a);
+    else hipLaunchKernelGGL((up_kernel<FT, 2, kOne, XT>), grid, dim3(64 * kWaves), 0, s, a);
     return hipGetLastError();
 }
 
@@ -463,6 +511,16 @@ hipError_t launch_adapters_add(const AdapterSet& set, const void* x, int x_dtype
     const int es = x_dtype == kF32 ? 4 : 2;
     const bool vec = (set.K * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
     const dim3 down((unsigned)(c.tiles * c.groups * set.rank_tiles * c.chunks)), block(64 * kWaves), up((unsigned)(c.tiles * c.col_groups));
+    // One launch where every workgroup can compute t in about the time of a launch: up to 256 KB of factors (us with the
+    // linear, K = N = 2048, rank 16, bf16: 1 row 10.7 against 13.9 in two launches, 4 rows 14.1 and 15.2, 8 rows, 512 KB,
+    // 17.9 and 16.6).
+    const int64_t again = M * set.rank_tiles * 32 * set.k_pad;
+    if (M <= 16 && set.rank_tiles <= 2 && vec && again <= (256 << 10)) {
+#define Q4GSW_ONE(FT) \
+    (x_dtype == kF32 ? one_launch<FT, kF32>(a, up, s) : (x_dtype == kF16 ? one_launch<FT, kF16>(a, up, s) : one_launch<FT, kBF16>(a, up, s)))
+        return set.dtype == kF16 ? Q4GSW_ONE(kF16) : Q4GSW_ONE(kBF16);
+#undef Q4GSW_ONE
+    }
     hipError_t e;
 #define Q4GSW_DOWN(FT)                                                                                        \
     x_dtype == kF32 ? down_launch<FT, kF32>(a, vec, down, block, s)                                           \

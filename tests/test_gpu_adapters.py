@@ -75,6 +75,11 @@ def some_slots(m, n, seed, runs=False):
 CASES = [
     # rows, K, N, rank, slots, x, factors, runs
     (1, 32, 32, 1, 1, BF16, BF16, False),
+    (1, 4096, 130, 32, 3, BF16, F16, False),                   # one launch: t in every workgroup
+    (3, 1024, 2049, 16, 2, F16, BF16, False),
+    (16, 256, 516, 20, 16, F32, F16, False),
+    (9, 512, 64, 16, 9, BF16, BF16, False),
+    (4, 2080, 100, 16, 2, F32, BF16, False),                   # just past it
     (1, 2048, 2048, 16, 8, F32, BF16, False),
     (2, 100, 7, 5, 3, F16, F16, False),
     (15, 33, 1, 16, 4, F32, F16, False),
