@@ -138,27 +138,30 @@ AttnPlan plan_rows(const AttnSize& n) {
     return p;
 }
 
-// us that a CU takes for a unit of 32 keys and 32 rows of a tree (one wave a SIMD at 256 channels).
-float tree_unit(int dim, bool prec) {
-    return (dim <= 192 ? 0.04f + 0.0017f * dim : 0.6f) * (prec ? 1.25f : 1.0f);
-}
-
-// Trees of more than 16 rows, tiles of 32.  VALU is the bound, so one workgroup of eight waves a CU (four at 256 channels) does as
-// well as more, and splits pay while they fill the CUs: us of 16 sequences of 1024 .. 4096 tokens, 32 / 8 heads of
-// 128, bf16 (fp16), 8 nodes (128 workgroups): 1 split 38 (47), 2 splits 27 (32), 4 splits 28 (32), 8 splits 33 (40);
-// 16 nodes (256): 39 (47), 42 (51), 46 (56), 51 (65); 64 nodes (1024): 88 (117), 98 (128); 17 blocks, heads of 64: 1
-// split 9.7, 2 splits 11.9.
-AttnPlan plan_tree(const AttnSize& n) {
+// Trees, in tiles of 16 rows (kv_rows) or of 32 (kv_tree), `most` waves a workgroup, `unit` us that a CU takes for a unit
+// of 32 keys and a tile.  VALU is the bound, so one workgroup of eight waves a CU does as well as more, and
+// splits pay while they fill the CUs: us of 16 sequences of 1024 .. 4096 tokens, 32 / 8 heads of 128, bf16 (fp16), in
+// tiles of 32, 8 nodes (128 workgroups): 1 split 38 (47), 2 splits 27 (32), 4 splits 28 (32), 8 splits 33 (40); 16
+// nodes (256): 39 (47), 42 (51), 46 (56), 51 (65); 64 nodes (1024): 88 (117), 98 (128).  In tiles of 16, 8 sequences of
+// 26 nodes, window 1024, 16 / 4 heads of 256 (224 workgroups): 1 split 24, 2 splits 32; up to 32 blocks none pay: 521
+// tokens, heads of 64: 1 split 9.2, 2 splits 13.7.
+AttnPlan plan_tiles(const AttnSize& n, int tile, int most, float unit, float start) {
     AttnPlan p{};
-    p.kernel = AttnPlan::kTree;
-    p.row_tiles = (n.rows + 31) / 32;
-    const int64_t groups = (int64_t)n.batch * n.heads * p.row_tiles, blocks = n.blocks(32);
+    p.row_tiles = (n.rows + tile - 1) / tile;
+    const int64_t groups = (int64_t)n.batch * n.heads * p.row_tiles, blocks = n.blocks(tile);
     int64_t splits = 1;
     if (blocks > 32) splits = kCus / groups < blocks / 8 ? kCus / groups : blocks / 8;
     finish_plan(p, n, blocks, splits);
-    p.waves = groups * p.splits <= kCus && kv_tree_most(n.dim) == 8 ? 8 : 4;
+    p.waves = groups * p.splits <= kCus ? most : 4;
     const float all = groups * n.mean / kCus, longest = (float)((p.chunk + p.waves - 1) / p.waves * p.waves);
-    p.us += 4.5f + 0.035f * n.dim + tree_unit(n.dim, n.prec) * (longest > all ? longest : all);
+    p.us += start + unit * (longest > all ? longest : all);
+    return p;
+}
+
+AttnPlan plan_tree(const AttnSize& n) {
+    const float unit = n.dim <= 192 ? 0.04f + 0.0017f * n.dim : 0.6f;       // one wave a SIMD at 256 channels
+    AttnPlan p = plan_tiles(n, 32, kv_tree_most(n.dim), unit * (n.prec ? 1.25f : 1.0f), 4.5f + 0.035f * n.dim);
+    p.kernel = AttnPlan::kTree;
     return p;
 }
 
@@ -229,10 +232,11 @@ AttnSize attention_size(int heads, int dim, int batch, int hq, int max_new, int 
 AttnPlan plan_attention(const AttnSize& n, int kernel) {
     if (kernel == Q4GSW_KV_MANY_ROWS) return plan_prompt(n);
     if (kernel == Q4GSW_KV_TREE) return plan_tree(n);
-    AttnPlan few = plan_rows(n);
+    AttnPlan few = n.tree ? plan_tiles(n, 16, 8, 0.06f + 0.00105f * n.dim, 4.0f + 0.02f * n.dim) : plan_rows(n);
     if (kernel == Q4GSW_KV_FEW_ROWS) return few;
-    // a tree's tiles of 32 rows cost a unit less VALU, tiles of 16 spread over more CUs and start sooner (16 nodes of 600
-    // tokens, 32 / 8 heads of 128, bf16: 11.9 us against 14.2; the batch of plan_tree's comment, 8 nodes: 33 against 28)
+    // a tree's tiles of 32 rows cost less VALU a row, tiles of 16 spread over more CUs and start sooner (us of 16 nodes of
+    // 600 tokens, 32 / 8 heads of 128, bf16: 10.5 against 14.2; the batch of plan_tiles' comment, 8 nodes: 31 against 27, 32
+    // nodes in fp16 77 and 81)
     if (n.tree && n.rows > 16) {
         const AttnPlan wide = plan_tree(n);
         if (wide.us < few.us) few = wide;

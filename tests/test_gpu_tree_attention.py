@@ -88,20 +88,24 @@ def test_places_of_the_tree(start, group, kernel):
         kernel=kernel)
 
 
-@pytest.mark.parametrize("kernel,news,lens,hq,hkv,dim", [
-    ("few_rows", [4, 2], [700, 64], 8, 2, 128), ("few_rows", [16, 9], [90, 333], 3, 3, 64),
-    ("many_rows", [9, 4], [700, 64], 8, 2, 128), ("many_rows", [70, 33], [200, 400], 4, 1, 64)])
-def test_a_chain_is_causal_attention(kernel, news, lens, hq, hkv, dim):
-    """Parents i - 1 give kv_attention's output bit for bit where one kernel serves both (up to 16 rows of a
-    cache head, or many): the same products in the same order."""
+@pytest.mark.parametrize("kernel,news,lens,hq,hkv,dim,same", [
+    ("few_rows", [4, 2], [700, 64], 8, 2, 128, False), ("few_rows", [16, 9], [90, 333], 3, 3, 64, True),
+    ("few_rows", [4, 2], [500, 64], 8, 2, 128, True),
+    ("many_rows", [9, 4], [700, 64], 8, 2, 128, True), ("many_rows", [70, 33], [200, 400], 4, 1, 64, True)])
+def test_a_chain_is_causal_attention(kernel, news, lens, hq, hkv, dim, same):
+    """Parents i - 1 give kv_attention's output: bit for bit where one kernel with one plan serves both (the same
+    products in the same order), else within the bound of either (trees split long caches less)."""
     q = lib()
-    cache, table, ln, _, _ = fill(q, lens, hkv, dim, 64, F16, 3)
+    cache, table, ln, keys, values = fill(q, lens, hkv, dim, 64, F16, 3)
     x = torch.randn(sum(news), hq, dim, generator=torch.Generator().manual_seed(1)).half().cuda()
     where = (table, offsets(news), ln, max(news), max(lens))
     with q.forced_kv_kernel(kernel):
         want = q.kv_attention(cache, x, *where)
         got = q.kv_tree_attention(cache, x, ints([i - 1 for n in news for i in range(n)]), *where)
-    assert torch.equal(got, want)
+    if same:
+        assert torch.equal(got, want)
+    bound = tree_attention(x.cpu(), keys, values, [forest(n, "chain") for n in news], lens)[1]
+    assert float(((got.double() - want.double()).abs().cpu() / bound).max()) <= 2
 
 
 def test_rows_without_keys_and_hidden_pages():
