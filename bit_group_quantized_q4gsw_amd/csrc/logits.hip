@@ -116,7 +116,7 @@ struct Rows {
         }
         if (first < 0) first = 0;
         end = min(min(end, first + a.max_new), a.rows);
-        return row < end;
+        return row >= first && row < end;                     // an offset may lie behind the next one
     }
 };
 

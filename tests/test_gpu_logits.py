@@ -218,3 +218,18 @@ def test_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         same(out, model(new, d)[0])
+
+
+def test_offsets_that_do_not_rise():
+    """An offset above the next one's: the rows before it are its sequence's no more, and no other's."""
+    q = lib()
+    logits, c = case(4, [5, 4, 0, 0], 700, F32, 30, seed=11)
+    c["cu"] = ints([0, 5, 9, 1, 9])
+    out = torch.full((9, 700), 7.0, device="cuda")
+    on = {k: (x.cuda() if isinstance(x, torch.Tensor) else x) for k, x in c.items()}
+    q.logits_adjust(logits.cuda(), **on, out=out)
+    one = {k: (x[:1] if k in ("repetition", "presence", "frequency", "history", "history_lens", "prompt_lens", "bias", "bias_ids",
+                              "ids", "parents", "mask") else x) for k, x in c.items()}
+    want, _ = model(logits[:1], dict(one, cu=ints([0, 1])))
+    same(out[:1], want)                                           # the first row is the first sequence's still
+    assert (out[1:] == 7.0).all()
