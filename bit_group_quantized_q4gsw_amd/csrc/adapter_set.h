@@ -48,5 +48,9 @@ hipError_t launch_adapters_load(const AdapterSet& set, int slot, const void* A, 
                                 hipStream_t s);
 hipError_t launch_adapters_add(const AdapterSet& set, const void* x, int x_dtype, int64_t M, const int32_t* slot, const float* y,
                                float* out, void* ws, hipStream_t s);
+// out = the sums of `splits` planes of partials [M rounded up to 32, width] in the fragment layout (internal.h)
+// + the adapters' terms; t: adapters_ws_bytes bytes beside the partials.
+hipError_t launch_adapters_join(const AdapterSet& set, const void* x, int x_dtype, int64_t M, const int32_t* slot, const float* part,
+                                int splits, int64_t width, float* out, void* t, hipStream_t s);
 
 }  // namespace q4gsw

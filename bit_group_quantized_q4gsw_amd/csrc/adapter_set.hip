@@ -11,6 +11,8 @@
 //   * out = y + alpha t B_s^T: factors as the first operand of the 16x16x16 product, so that a lane ends
 //     with eight neighbouring columns of one row.  With few rows the waves of a workgroup share the adapters of
 //     16 rows (a row is its adapter's wave's alone), with many they share the columns.
+// Beside a linear whose K is split, the launch that sums the splits adds the terms (adapters_fwd, 64 rows of 32 adapters,
+// K = 2048, N = 8192: 24 us against 27 with the sum in a launch of its own).
 // Few rows of small factors take one launch, in which every workgroup of the second computes t itself.
 // Rows need no order: adapters are found among each 16 rows by comparison, and one that many tiles share
 // is read from L2 by all but the first.
@@ -211,6 +213,47 @@ __global__ __launch_bounds__(64 * kWaves) void down_kernel(AdapterArgs a) {
     }
 }
 
+// t of row m, ranks 16 s + 4 q .. + 3: its chunks in order.
+template <int S>
+__device__ __forceinline__ void row_terms(const AdapterArgs& a, int64_t m, int q, f4 (&tv)[S]) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const float* t = a.t + m * (16 * S) + 16 * s + 4 * q;
+        f4 v[kMostChunks];
+#pragma unroll
+        for (int c = 0; c < kMostChunks; ++c) v[c] = *reinterpret_cast<const f4*>(t + min(c, a.chunks - 1) * a.M * (16 * S));
+        tv[s] = v[0];
+#pragma unroll
+        for (int c = 1; c < kMostChunks; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tv[s][e] += c < a.chunks ? v[c][e] : 0.0f;
+    }
+}
+
+// alpha t as the parts of an operand; the factor that the products take then (fp16 factors).
+template <int FT, int S, int P>
+__device__ __forceinline__ float term_parts(f4 (&tv)[S], float alpha, u2 (&part)[S][P]) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            tv[s][e] *= alpha;
+            amax = fmaxf(amax, fabsf(tv[s][e]));
+        }
+    float mul = 1.0f, inv = 1.0f;
+    if constexpr (FT == kF16) row_factor(wave_max_rows(amax), mul, inv);
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float v0 = tv[s][2 * e] * mul, v1 = tv[s][2 * e + 1] * mul;
+#pragma unroll
+            for (int p = 0; p < P; ++p) part[s][p][e] = take_part<FT>(v0, v1);
+        }
+    return inv;
+}
+
 // out = y + alpha t B^T for 16 rows, S steps of 16 ranks.  kMany: 256 columns, 64 a wave.  kFew: 32 J columns,
 // the adapters of the rows dealt to the waves.  kOne: as kFew, of one tile of rows, and t is computed here, by every
 // workgroup once more (XT: the rows' type, which the others do not look at).
@@ -274,18 +317,7 @@ __global__ __launch_bounds__(KIND == kOne ? 64 * kWaves : 256) void up_kernel(Ad
         if (mine >= 0) alpha = a.set.alpha[mine];
         if (!__any(here)) return;
     } else if (here && mine >= 0) {
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const float* t = a.t + m * (16 * S) + 16 * s + 4 * q;
-            f4 v[kMostChunks];
-#pragma unroll
-            for (int c = 0; c < kMostChunks; ++c) v[c] = *reinterpret_cast<const f4*>(t + min(c, a.chunks - 1) * a.M * (16 * S));
-            tv[s] = v[0];
-#pragma unroll
-            for (int c = 1; c < kMostChunks; ++c)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) tv[s][e] += c < a.chunks ? v[c][e] : 0.0f;
-        }
+        row_terms<S>(a, m, q, tv);
         alpha = a.set.alpha[mine];
     }
     f4 acc[J][2], base[J][2];
@@ -325,25 +357,8 @@ __global__ __launch_bounds__(KIND == kOne ? 64 * kWaves : 256) void up_kernel(Ad
     };
     fetch();
 
-    float amax = 0.0f;
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            tv[s][e] *= alpha;
-            amax = fmaxf(amax, fabsf(tv[s][e]));
-        }
-    float mul = 1.0f, inv = 1.0f;
-    if constexpr (FT == kF16) row_factor(wave_max_rows(amax), mul, inv);
     u2 part[S][P];
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float v0 = tv[s][2 * e] * mul, v1 = tv[s][2 * e + 1] * mul;
-#pragma unroll
-            for (int p = 0; p < P; ++p) part[s][p][e] = take_part<FT>(v0, v1);
-        }
+    const float inv = term_parts<FT, S, P>(tv, alpha, part);
 
     for (; slot[0] >= 0; fetch()) {
 #pragma unroll
@@ -385,6 +400,103 @@ __global__ __launch_bounds__(KIND == kOne ? 64 * kWaves : 256) void up_kernel(Ad
                     if (n + e < a.N) a.out[m * a.N + n + e] = v[e];
             }
         }
+}
+
+// The sums of a projection's K splits and the adapters' terms in one launch: a workgroup takes a 32x32 tile of
+// the partials (fragment layout, internal.h), a wave 16 rows and half the columns of it.  Roles are swapped against
+// up_kernel: t is the first operand, so that a lane ends with four rows of one column, as the partials lie.
+template <int FT, int S>
+__global__ __launch_bounds__(256) void join_kernel(AdapterArgs a, const float* __restrict__ part, int splits, int64_t ntn,
+                                                   int64_t plane) {
+    constexpr int P = FT == kF16 ? 2 : 3;
+    constexpr int kBatch = 8 / S > 2 ? 8 / S : 2;         // adapters whose factors are loaded together
+    constexpr int kPlanes = 4;                            // partials loaded together
+    __shared__ float s_tile[32][33];
+    const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), mh = wave >> 1, h = wave & 1;
+    const int64_t tm = blockIdx.x / ntn, tn = blockIdx.x % ntn;
+    if (32 * tn >= a.N) return;                           // columns that only the packed weight has
+    const float* src = part + (int64_t)blockIdx.x * 1024 + 4 * (64 * (2 * mh + (q >> 1)) + 32 * (q & 1) + adapter_col(i, h));
+    f4 p[kPlanes];
+#pragma unroll
+    for (int k = 0; k < kPlanes; ++k) p[k] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(src + (k < splits ? k : 0) * plane));
+
+    const int64_t m = 32 * tm + 16 * mh + i;
+    const int mine = row_slot(a, 2 * tm + mh, i);
+    uint32_t firsts = first_rows(mine, i);
+    f4 tv[S];
+    float alpha = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) tv[s] = f4{0.f, 0.f, 0.f, 0.f};
+    if (mine >= 0) {
+        row_terms<S>(a, m, q, tv);
+        alpha = a.set.alpha[mine];
+    }
+    u2 b[kBatch][S];
+    int slot[kBatch];
+    auto fetch = [&]() {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            slot[k] = -1;
+            if (!firsts) continue;
+            slot[k] = __builtin_amdgcn_readlane(mine, __builtin_ctz(firsts));
+            firsts &= firsts - 1;
+            const uint8_t* B = a.set.data + slot[k] * a.set.slot_bytes + a.set.b_offset + tn * S * 1024 + 16 * lane + 8 * h;
+#pragma unroll
+            for (int s = 0; s < S; ++s) b[k][s] = *reinterpret_cast<const u2*>(B + 1024 * s);
+        }
+    };
+    fetch();
+
+    f4 sum = p[0];
+#pragma unroll
+    for (int k = 1; k < kPlanes; ++k)
+        if (k < splits) sum += p[k];
+    for (int s0 = kPlanes; s0 < splits; s0 += kPlanes) {
+#pragma unroll
+        for (int k = 0; k < kPlanes; ++k)
+            p[k] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(src + (s0 + k < splits ? s0 + k : 0) * plane));
+#pragma unroll
+        for (int k = 0; k < kPlanes; ++k)
+            if (s0 + k < splits) sum += p[k];
+    }
+
+    u2 parts[S][P];
+    const float inv = term_parts<FT, S, P>(tv, alpha, parts);
+    int of[4];                                            // slots of the lane's rows
+#pragma unroll
+    for (int e = 0; e < 4; ++e) of[e] = __shfl(mine, 4 * q + e);
+    f4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (; slot[0] >= 0; fetch()) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (slot[k] < 0) break;
+            f4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int e = 0; e < P; ++e) d = mfma16<FT>(parts[s][e], b[k][s], d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = of[e] == slot[k] ? d[e] : acc[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float f = FT == kF16 ? __shfl(inv, 4 * q + e) : 1.0f;
+        s_tile[16 * mh + 4 * q + e][adapter_col(i, h)] = of[e] < 0 ? sum[e] : (FT == kF16 ? fmaf(acc[e], f, sum[e]) : sum[e] + acc[e]);
+    }
+    __syncthreads();
+    const int row = tid >> 3, c4 = 4 * (tid & 7);
+    const int64_t mo = 32 * tm + row, n = 32 * tn + c4;
+    if (mo >= a.M) return;
+    float* dst = a.out + mo * a.N + n;
+    if (a.quads) {
+        if (n < a.N) *reinterpret_cast<f4*>(dst) = f4{s_tile[row][c4], s_tile[row][c4 + 1], s_tile[row][c4 + 2], s_tile[row][c4 + 3]};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) dst[e] = s_tile[row][c4 + e];
+    }
 }
 
 // One slot's factors into the set, 16 bytes a thread, and its alpha; zeros past rank, K and N.
@@ -503,33 +615,76 @@ hipError_t launch_adapters_load(const AdapterSet& set, int slot, const void* A, 
     return hipGetLastError();
 }
 
+namespace {
+
+AdapterArgs args_of(const AdapterSet& set, const Cut& c, const void* x, int64_t M, const int32_t* slot, const float* y, float* out,
+                    void* t) {
+    AdapterArgs a{set, x, M, set.K, set.N, slot, y, out, static_cast<float*>(t), c.chunks, c.groups, set.rank_tiles, c.col_groups, false};
+    a.quads = set.N % 4 == 0 && ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+    return a;
+}
+
+// rows of x hold aligned octets
+bool octets(const AdapterSet& set, const void* x, int x_dtype) {
+    return (set.K * (x_dtype == kF32 ? 4 : 2)) % 16 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
+}
+
+hipError_t launch_down(const AdapterArgs& a, const Cut& c, int x_dtype, hipStream_t s) {
+    const dim3 down((unsigned)(c.tiles * c.groups * a.rank_tiles * c.chunks)), block(64 * kWaves);
+    const bool vec = octets(a.set, a.x, x_dtype);
+#define Q4GSW_DOWN(FT)                                                                                        \
+    (x_dtype == kF32 ? down_launch<FT, kF32>(a, vec, down, block, s)                                          \
+                     : (x_dtype == kF16 ? down_launch<FT, kF16>(a, vec, down, block, s) : down_launch<FT, kBF16>(a, vec, down, block, s)))
+    return a.set.dtype == kF16 ? Q4GSW_DOWN(kF16) : Q4GSW_DOWN(kBF16);
+#undef Q4GSW_DOWN
+}
+
+template <int FT>
+hipError_t join_launch(const AdapterArgs& a, const float* part, int splits, int64_t width, hipStream_t s) {
+    const dim3 grid((unsigned)((a.M + 31) / 32 * (width / 32)));
+    const int64_t plane = frag_plane_floats(a.M, width);
+#define Q4GSW_JOIN(S) \
+    case S: hipLaunchKernelGGL((join_kernel<FT, S>), grid, dim3(256), 0, s, a, part, splits, width / 32, plane); break;
+    switch (a.rank_tiles) {
+        Q4GSW_JOIN(1)
+        Q4GSW_JOIN(2)
+        Q4GSW_JOIN(3)
+        Q4GSW_JOIN(4)
+        default: return hipErrorInvalidValue;
+    }
+#undef Q4GSW_JOIN
+    return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_adapters_add(const AdapterSet& set, const void* x, int x_dtype, int64_t M, const int32_t* slot, const float* y,
                                float* out, void* ws, hipStream_t s) {
     const Cut c = cut_of(set, M);
-    AdapterArgs a{set, x, M, set.K, set.N, slot, y, out, static_cast<float*>(ws), c.chunks, c.groups, set.rank_tiles, c.col_groups, false};
-    a.quads = set.N % 4 == 0 && ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
-    const int es = x_dtype == kF32 ? 4 : 2;
-    const bool vec = (set.K * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
-    const dim3 down((unsigned)(c.tiles * c.groups * set.rank_tiles * c.chunks)), block(64 * kWaves), up((unsigned)(c.tiles * c.col_groups));
+    const AdapterArgs a = args_of(set, c, x, M, slot, y, out, ws);
+    const dim3 up((unsigned)(c.tiles * c.col_groups));
     // One launch where every workgroup can compute t in about the time of a launch: up to 256 KB of factors (us with the
     // linear, K = N = 2048, rank 16, bf16: 1 row 10.7 against 13.9 in two launches, 4 rows 14.1 and 15.2, 8 rows, 512 KB,
     // 17.9 and 16.6).
     const int64_t again = M * set.rank_tiles * 32 * set.k_pad;
-    if (M <= 16 && set.rank_tiles <= 2 && vec && again <= (256 << 10)) {
+    if (M <= 16 && set.rank_tiles <= 2 && octets(set, x, x_dtype) && again <= (256 << 10)) {
 #define Q4GSW_ONE(FT) \
     (x_dtype == kF32 ? one_launch<FT, kF32>(a, up, s) : (x_dtype == kF16 ? one_launch<FT, kF16>(a, up, s) : one_launch<FT, kBF16>(a, up, s)))
         return set.dtype == kF16 ? Q4GSW_ONE(kF16) : Q4GSW_ONE(kBF16);
 #undef Q4GSW_ONE
     }
-    hipError_t e;
-#define Q4GSW_DOWN(FT)                                                                                        \
-    x_dtype == kF32 ? down_launch<FT, kF32>(a, vec, down, block, s)                                           \
-                    : (x_dtype == kF16 ? down_launch<FT, kF16>(a, vec, down, block, s) : down_launch<FT, kBF16>(a, vec, down, block, s))
-    if (set.dtype == kF16) e = Q4GSW_DOWN(kF16);
-    else e = Q4GSW_DOWN(kBF16);
-#undef Q4GSW_DOWN
+    const hipError_t e = launch_down(a, c, x_dtype, s);
     if (e != hipSuccess) return e;
     return set.dtype == kF16 ? up_launch<kF16>(a, c.many, up, s) : up_launch<kBF16>(a, c.many, up, s);
+}
+
+hipError_t launch_adapters_join(const AdapterSet& set, const void* x, int x_dtype, int64_t M, const int32_t* slot, const float* part,
+                                int splits, int64_t width, float* out, void* t, hipStream_t s) {
+    const Cut c = cut_of(set, M);
+    const AdapterArgs a = args_of(set, c, x, M, slot, out, out, t);
+    const hipError_t e = launch_down(a, c, x_dtype, s);
+    if (e != hipSuccess) return e;
+    return set.dtype == kF16 ? join_launch<kF16>(a, part, splits, width, s) : join_launch<kBF16>(a, part, splits, width, s);
 }
 
 }  // namespace q4gsw

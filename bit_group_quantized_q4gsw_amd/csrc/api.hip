@@ -315,6 +315,16 @@ q4gsw_status set_shape(const q4gsw_adapters* a, AdapterSet* v, uint64_t* need) {
     return Q4GSW_OK;
 }
 
+// The MFMA forward's plan where it splits K; else splits is 0.
+FwdPlan split_gemm(const q4gsw_weight* w, int64_t M, int32_t dt, int32_t route) {
+    if (route != Q4GSW_ROUTE_GEMM_FOLD && route != Q4GSW_ROUTE_GEMM_GROUP && route != Q4GSW_ROUTE_GEMM_SPLIT) return FwdPlan{};
+    FwdSeg seg{view_of(w), nullptr};
+    const FwdPlan plan = plan_gemm_fwd(&seg, 1, dt, fold_ok(w), M);
+    return plan.splits > 1 ? plan : FwdPlan{};
+}
+
+uint64_t beside(uint64_t bytes) { return (uint64_t)round_up((int64_t)bytes, 256); }
+
 q4gsw_status check_set(const q4gsw_adapters* a, AdapterSet* v, Range* r) {
     uint64_t need = 0;
     const q4gsw_status st = set_shape(a, v, &need);
@@ -932,6 +942,10 @@ q4gsw_status q4gsw_adapters_workspace_bytes(const q4gsw_adapters* set, const q4g
         const int32_t route = pick_fwd(w, M, x_dtype, false, Q4GSW_ROUTE_NONE, &st);
         if (st != Q4GSW_OK) return st;
         base = fwd_ws_bytes(w, M, x_dtype, route, Opts());
+        if (split_gemm(w, M, x_dtype, route).splits > 1) {
+            *bytes = beside(base) + adapters_ws_bytes(v, M);
+            return Q4GSW_OK;
+        }
     }
     // the linear's workspace is free again when the adapters' launches begin
     *bytes = adapters_ws_bytes(v, M);
@@ -973,12 +987,22 @@ q4gsw_status q4gsw_adapters_fwd(const q4gsw_weight* w, const q4gsw_adapters* set
     if ((st = check_set(set, &v, &sr)) != Q4GSW_OK) return st;
     if (!slot) return Q4GSW_E_NULL;
     if (w->N != v.N || w->K != v.K || !adapters_launch_ok(v, M)) return Q4GSW_E_SHAPE;
-    const uint64_t terms = adapters_ws_bytes(v, M), need = base > terms ? base : terms;
+    const FwdPlan plan = split_gemm(w, M, x_dtype, route);
+    const uint64_t terms = adapters_ws_bytes(v, M), need = plan.splits > 1 ? beside(base) + terms : (base > terms ? base : terms);
     if (!ws_ok(ws, ws_bytes, need)) return Q4GSW_E_WORKSPACE;
     if ((st = fwd_alias(w, x, x_dtype, M, y, ws, need)) != Q4GSW_OK) return st;
     const Range yr = range_of(y, (uint64_t)M * w->N * 4), wr = range_of(ws, need), ir = range_of(slot, (uint64_t)M * 4);
     if (overlap(yr, sr) || overlap(wr, sr) || overlap(yr, ir) || overlap(wr, ir)) return Q4GSW_E_ALIAS;
     hipStream_t s = static_cast<hipStream_t>(stream);
+    if (plan.splits > 1) {
+        // the launch that sums the splits adds the adapters' terms
+        FwdSeg seg{view_of(w), y};
+        float* part = static_cast<float*>(ws);
+        const hipError_t e = launch_gemm_fwd(&seg, 1, x, x_dtype, M, plan, part, s, nullptr, nullptr, false);
+        if (e != hipSuccess) return hip_status(e);
+        return hip_status(launch_adapters_join(v, x, x_dtype, M, slot, part, plan.splits, seg.w.n_pad, y,
+                                               static_cast<uint8_t*>(ws) + beside(base), s));
+    }
     if ((st = run_fwd(w, x, x_dtype, M, y, ws, route, o, s)) != Q4GSW_OK) return st;
     return hip_status(launch_adapters_add(v, x, x_dtype, M, slot, y, y, ws, s));
 }

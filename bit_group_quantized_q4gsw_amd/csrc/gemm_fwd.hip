@@ -847,7 +847,8 @@ FwdPlan plan_gemm_fwd(const FwdSeg* segs, int nseg, int x_dtype, int fold_ok, in
 // One launch over every segment.  With K splits the partials go to ws as splits planes in the
 // fragment layout over the columns of all segments (segment i from column sum_{j<i} n_pad_j on).
 hipError_t launch_gemm_fwd(const FwdSeg* segs, int nseg, const void* x, int x_dtype, int64_t M,
-                           const FwdPlan& plan, float* ws, hipStream_t s, const LowRankEpi* lr, bool* lr_done) {
+                           const FwdPlan& plan, float* ws, hipStream_t s, const LowRankEpi* lr, bool* lr_done,
+                           bool reduce) {
     if (lr_done) *lr_done = false;
     const WView& w0 = segs[0].w;
     FwdSegArgs a{};
@@ -920,7 +921,7 @@ hipError_t launch_gemm_fwd(const FwdSeg* segs, int nseg, const void* x, int x_dt
     if (!launched) return hipErrorInvalidValue;
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && in_kernel && lr_done) *lr_done = true;
-    if (e != hipSuccess || plan.splits == 1) return e;
+    if (e != hipSuccess || plan.splits == 1 || !reduce) return e;
     if (lr && lr_done) *lr_done = true;
     const float* ys[3];
     int64_t yld[3], off[3], cols[3];

@@ -112,9 +112,10 @@ bool gemm_fwd_supported(const WView& w, int x_dtype, int fold_ok);
 // operations in the same order as the separate expansion) or, with one split, by the exact-code
 // group instances with 128-column chunks and fp16 scales in their epilogue (fp32 MFMAs into the
 // accumulators); *lr_done tells whether this launch applied it.
+// reduce false: partials stay in ws for the caller to sum.
 hipError_t launch_gemm_fwd(const FwdSeg* segs, int nseg, const void* x, int x_dtype, int64_t M,
                            const FwdPlan& plan, float* ws, hipStream_t s, const LowRankEpi* lr = nullptr,
-                           bool* lr_done = nullptr);
+                           bool* lr_done = nullptr, bool reduce = true);
 
 // MFMA input gradient: gemm_bwd2.hip (32x32x16) dispatches, gemm_bwd.hip (16x16x32) covers
 // the group sizes the former does not take.

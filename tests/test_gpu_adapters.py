@@ -263,3 +263,35 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         want, bound = formula(y.cpu(), x.cpu(), ad, now, BF16)
         check(out, want, bound, f"replay {step}")
+
+
+@pytest.mark.parametrize("ftype", [F16, BF16])
+@pytest.mark.parametrize("m,n,k,rank,slots,xtype", [
+    (9, 64, 512, 5, 3, BF16),
+    (17, 96, 1024, 16, 20, F16),
+    (33, 65, 640, 24, 40, BF16),                   # odd columns, a tile with one row
+    (64, 2050, 2048, 33, 70, F32),
+    (50, 1000, 4096, 64, 8, F16),
+    (200, 512, 4480, 16, 3, BF16),                 # three chunks of K
+    (31, 320, 8192, 48, 64, F32),
+])
+def test_in_the_sum_of_a_split_linear(m, n, k, rank, slots, xtype, ftype):
+    """Where the linear splits K, adapters_fwd adds the terms in the launch that sums the splits: the same values."""
+    q = lib()
+    g = torch.Generator().manual_seed(m)
+    w = q.pack(torch.randint(0, 16, (n, k), generator=g, dtype=torch.uint8).cuda(),
+               (0.01 + 0.01 * torch.rand(k // 32, n, generator=g)).half().cuda(), 32)
+    ad = factors(slots, rank, n, k, ftype, seed=1, ranks=[rank, 1 + rank // 2])
+    s = make(q, ad, rank, n, k, ftype)
+    x, at = torch.randn(m, k, generator=g).to(xtype), some_slots(m, slots, 1)
+    y = q.linear_fwd(w, x.cuda())
+    ws = torch.full((q.adapters_workspace_bytes(s, m, xtype, w),), 0xFF, dtype=torch.uint8, device="cuda")
+    got = q.adapters_fwd(w, x.cuda(), s, ints(at), workspace=ws)
+    assert torch.equal(got, q.adapters_add(y, x.cuda(), s, ints(at)))
+    want, bound = formula(y.cpu(), x, ad, at, ftype)
+    check(got, want, bound, f"split {m} {n} {k}")
+    # a row's term that is not finite stays in its row
+    x[m // 2, 3] = float("nan")
+    got = q.adapters_fwd(w, x.cuda(), s, ints(at))
+    keep = torch.arange(m) != m // 2
+    assert torch.equal(got.cpu()[keep], q.adapters_add(y, x.cuda(), s, ints(at)).cpu()[keep])
