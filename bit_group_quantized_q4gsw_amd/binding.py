@@ -127,11 +127,12 @@ def _opts():
 
 
 _lib: Optional[ctypes.CDLL] = None
+_host = None            # the module _host: regular serving calls, marshalled in C++ (csrc/host.cpp)
 
 
 def lib() -> ctypes.CDLL:
     """The loaded library; raises if it has not been built (no fallback exists)."""
-    global _lib
+    global _lib, _host
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing: build it with python bit_group_quantized_q4gsw_amd/build.py; "
@@ -204,7 +205,9 @@ def lib() -> ctypes.CDLL:
         h.q4gsw_layout_version.restype = ctypes.c_uint32
         h.q4gsw_build_info.argtypes = []
         h.q4gsw_build_info.restype = ctypes.c_char_p
-        _lib = h
+        from . import _host as host
+        host.open(h._handle, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        _lib, _host = h, host
     return _lib
 
 
@@ -219,6 +222,13 @@ def route_name(route: int) -> str:
 def _check(status: int, what: str) -> None:
     if status != 0:
         raise Q4gswError(status, what)
+
+
+def _done(result, what: str):
+    """What a function of _host returned, unless it is the status of a call that the library refused."""
+    if type(result) is int:
+        raise Q4gswError(result, what)
+    return result
 
 
 def _stream() -> int:
@@ -501,6 +511,7 @@ class KvCache:
         self.buffer = buffer
         self.pages, self.page_size, self.heads, self.dim = desc.pages, desc.page_size, desc.heads, desc.dim
         self._ref = ctypes.byref(desc)
+        self._addr = ctypes.addressof(desc)
         self._dev = buffer.get_device()
 
 
@@ -573,6 +584,9 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, table: torch.Ten
               lens: torch.Tensor) -> None:
     """Store the keys and values k, v [tokens, heads, dim] of new tokens: rows cu[b] .. cu[b + 1] - 1
     are the last of sequence b's lens[b] tokens (with them), whose pages are table[b]."""
+    done = _host.append(cache._addr, cache._dev, k, v, table, cu, lens)
+    if done is not None:
+        return _check(done, "q4gsw_kv_append")
     k, kp, k_ld, dt = _token_rows(k, cache.heads, cache, "k")
     v, vp, v_ld, v_dt = _token_rows(v, cache.heads, cache, "v")
     tokens = k.shape[0]
@@ -586,6 +600,10 @@ def kv_read(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, lens: torch.T
             out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(k, v) fp32 [tokens, heads, dim]: what the cache stands for at the places kv_append with the
     same table, cu and lens writes."""
+    if out is None:
+        done = _host.read(cache._addr, cache._dev, table, cu, lens, tokens)
+        if done is not None:
+            return _done(done, "q4gsw_kv_read")
     seqs = _kv_seqs(cache, table, cu, lens, tokens)
     dev = cache.buffer.device
     shape = (tokens, cache.heads, cache.dim)
@@ -638,6 +656,10 @@ def kv_attention(cache: KvCache, q: torch.Tensor, table: torch.Tensor, cu: torch
     lengths; window > 0 keeps the last `window` keys of each token, softcap > 0 caps the scores.  A row that
     sees no key gives zeros, else one whose query holds a NaN or an infinity gives NaN.  With `parents` the new tokens form a tree
     (kv_tree_attention)."""
+    if _local.kv is None:
+        done = _host.attention(cache._addr, cache._dev, q, parents, table, cu, lens, max_new, max_ctx, window, softcap, out, workspace)
+        if done is not None:
+            return _done(done, "q4gsw_kv_attention" if parents is None else "q4gsw_kv_tree_attention")
     if (max_new | max_ctx | window) >> 31:       # negative ones too, of which the library refuses the 32-bit ones
         _int32(max_new, max_ctx, window)
     if q.dim() != 3:
@@ -706,6 +728,9 @@ def kv_keep(caches, parents: torch.Tensor, leaf: torch.Tensor, table: torch.Tens
     for c in caches:
         if c._dev != first._dev:
             raise ValueError("caches must be on one device")
+    done = _host.keep([c._addr for c in caches], first._dev, parents, leaf, table, cu, lens, max_new, kept, path)
+    if done is not None:
+        return _done(done, "q4gsw_kv_keep")
     _int32(max_new)
     if max_new < 1:
         raise ValueError("max_new must be positive")
@@ -761,6 +786,10 @@ def logits_adjust(logits: torch.Tensor, cu: Optional[torch.Tensor] = None, max_n
     last counts.  Per row: ids (int32 [rows]), the rows' own tokens, which count as generated with those of the
     rows before them in the sequence, or with parents (as in kv_tree_attention) with those of their
     ancestors; mask (int32 [rows, ceil(V / 32)]), bit v % 32 of word v // 32 allows token v."""
+    done = _host.logits(logits, cu, max_new, history, history_lens, prompt_lens, ids, parents, repetition, presence, frequency,
+                        bias_ids, bias, mask, out)
+    if done is not None:
+        return _done(done, "q4gsw_logits_adjust")
     code = _TORCH_DTYPE.get(logits.dtype)
     dev = logits.get_device()
     if logits.dim() != 2 or code is None or dev < 0:
@@ -892,6 +921,7 @@ class Adapters:
         self.buffer = buffer
         self.slots, self.rank, self.N, self.K = desc.slots, desc.rank, desc.N, desc.K
         self._ref = ctypes.byref(desc)
+        self._addr = ctypes.addressof(desc)
         self._dev = buffer.get_device()
 
 
@@ -945,6 +975,9 @@ def adapters_fwd(w: PackedWeight, x: torch.Tensor, s: Adapters, slots: torch.Ten
                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [M, N] fp32: y[m] = x[m] . dequant(W)^T + alpha_i (x[m] A_i^T) B_i^T for the adapter in slot i = slots[m]
     (int32 [M]; outside the set's slots: none)."""
+    done = _host.adapters(ctypes.addressof(w.desc), s._addr, s._dev, x, slots, None, out, workspace)
+    if done is not None:
+        return _done(done, "q4gsw_adapters_fwd")
     x, code, slots, M = _adapter_rows(x, s, slots)
     y = _out(out, (M, s.N), x.device, "out")
     need = adapters_workspace_bytes(s, M, x.dtype, w)
@@ -958,6 +991,9 @@ def adapters_add(y: torch.Tensor, x: torch.Tensor, s: Adapters, slots: torch.Ten
                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """out [M, N] fp32: y[m] (fp32; a projection of the same rows) + alpha_i (x[m] A_i^T) B_i^T for the adapter in
     slot i = slots[m].  `out` may be y itself."""
+    done = _host.adapters(0, s._addr, s._dev, x, slots, y, out, workspace)
+    if done is not None:
+        return _done(done, "q4gsw_adapters_add")
     x, code, slots, M = _adapter_rows(x, s, slots)
     if y.dtype is not torch.float32 or tuple(y.shape) != (M, s.N) or y.get_device() != s._dev:
         raise ValueError(f"y must be an fp32 tensor [{M}, {s.N}] on {s.buffer.device}")
