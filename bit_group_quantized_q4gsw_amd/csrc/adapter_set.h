@@ -39,6 +39,7 @@ struct AdapterArgs {
     int rank_tiles;
     int64_t col_groups;
     bool quads;              // rows of y and out hold aligned quads
+    int share;               // waves that share a chunk of K
 };
 
 bool adapters_launch_ok(const AdapterSet& set, int64_t M);

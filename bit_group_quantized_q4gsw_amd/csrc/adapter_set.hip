@@ -193,8 +193,9 @@ __global__ __launch_bounds__(64 * kWaves) void down_kernel(AdapterArgs a) {
     const int mine = row_slot(a, tile, i);
     uint32_t firsts = first_rows(mine, i);
     const int64_t m = 16 * tile + i, row = m * a.K;
-    const int64_t steps = a.set.k_pad >> 5, parts = a.chunks * kWaves, per = (steps + parts - 1) / parts;
-    const int64_t begin = per * (chunk * kWaves + wave), s1 = min(begin + per, steps);
+    // the waves from a.share on have none of it, so that one launch for few rows sums in the same order
+    const int64_t steps = a.set.k_pad >> 5, parts = a.chunks * a.share, per = (steps + parts - 1) / parts;
+    const int64_t begin = wave < a.share ? per * (chunk * a.share + wave) : steps, s1 = min(begin + per, steps);
     for (int n = 0; firsts; firsts &= firsts - 1, ++n) {
         if (n % a.groups != group) continue;
         const int slot = __builtin_amdgcn_readlane(mine, __builtin_ctz(firsts));
@@ -286,40 +287,8 @@ __global__ __launch_bounds__(KIND == kOne ? 64 * kWaves : 256) void up_kernel(Ad
         if (KIND != kOne && !__any(here)) return;
     }
 
-    // t and what the columns hold so far
-    f4 tv[S];
-    float alpha = 0.0f;
-#pragma unroll
-    for (int s = 0; s < S; ++s) tv[s] = f4{0.f, 0.f, 0.f, 0.f};
-    if constexpr (KIND == kOne) {
-        __shared__ f4 s_t[kWaves][S][64];
-        const int64_t steps = a.set.k_pad >> 5, per = (steps + kWaves - 1) / kWaves;
-        for (uint32_t left = first_rows(mine, i); left; left &= left - 1) {
-            const int slot = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
-            const bool match = mine == slot;
-            const uint8_t* A = a.set.data + slot * a.set.slot_bytes + 16 * lane;
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                s_t[wave][s][lane] = down_part<FT, XT, true>(a, A + 1024 * s, 1024 * S, m * a.K, match, q, per * wave, min(per * (wave + 1), steps));
-            __syncthreads();
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                f4 t = s_t[0][s][lane];
-#pragma unroll
-                for (int w = 1; w < kWaves; ++w)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) t[e] += s_t[w][s][lane][e];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) tv[s][e] = match ? t[e] : tv[s][e];
-            }
-            __syncthreads();
-        }
-        if (mine >= 0) alpha = a.set.alpha[mine];
-        if (!__any(here)) return;
-    } else if (here && mine >= 0) {
-        row_terms<S>(a, m, q, tv);
-        alpha = a.set.alpha[mine];
-    }
+    // ---- what the columns hold so far and the first factors: on their way while t is computed ----
+    const float alpha = mine >= 0 ? a.set.alpha[mine] : 0.0f;
     f4 acc[J][2], base[J][2];
     auto col = [&](int j, int h) -> int64_t { return 32 * (blk0 + j) + 8 * q + 4 * h; };
 #pragma unroll
@@ -357,6 +326,50 @@ __global__ __launch_bounds__(KIND == kOne ? 64 * kWaves : 256) void up_kernel(Ad
     };
     fetch();
 
+    // ---- t ----
+    f4 tv[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) tv[s] = f4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (KIND == kOne) {
+        // a.share waves take one adapter's K, the others the next adapters'
+        __shared__ f4 s_t[kWaves][S][64];
+        const int ways = kWaves / a.share, way = wave / a.share;
+        const int64_t steps = a.set.k_pad >> 5, per = (steps + a.share - 1) / a.share, begin = per * (wave % a.share);
+        int first = 0;
+#pragma unroll
+        for (int j = 15; j >= 0; --j) first = __builtin_amdgcn_readlane(mine, j) == mine ? j : first;
+        uint32_t left = first_rows(mine, i);
+        int order = mine >= 0 ? __popc(left & ((1u << first) - 1u)) : -1;     // of the row's adapter
+        for (; left; order -= ways) {
+            uint32_t one = 0u;                                // the wave's adapter of this round
+            for (int w = 0; w < ways; ++w) {
+                const uint32_t low = left & (0u - left);
+                one = w == way ? low : one;
+                left ^= low;
+            }
+            if (one) {
+                const int slot = __builtin_amdgcn_readlane(mine, __builtin_ctz(one));
+                const uint8_t* A = a.set.data + slot * a.set.slot_bytes + 16 * lane;
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    s_t[wave][s][lane] = down_part<FT, XT, true>(a, A + 1024 * s, 1024 * S, m * a.K, mine == slot, q, begin, min(begin + per, steps));
+            }
+            __syncthreads();
+            if (order >= 0 && order < ways) {
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    tv[s] = s_t[order * a.share][s][lane];
+                    for (int w = 1; w < a.share; ++w)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) tv[s][e] += s_t[order * a.share + w][s][lane][e];
+                }
+            }
+            __syncthreads();
+        }
+        if (!__any(here)) return;
+    } else if (here && mine >= 0) {
+        row_terms<S>(a, m, q, tv);
+    }
     u2 part[S][P];
     const float inv = term_parts<FT, S, P>(tv, alpha, part);
 
@@ -619,7 +632,10 @@ namespace {
 
 AdapterArgs args_of(const AdapterSet& set, const Cut& c, const void* x, int64_t M, const int32_t* slot, const float* y, float* out,
                     void* t) {
-    AdapterArgs a{set, x, M, set.K, set.N, slot, y, out, static_cast<float*>(t), c.chunks, c.groups, set.rank_tiles, c.col_groups, false};
+    AdapterArgs a{set, x, M, set.K, set.N, slot, y, out, static_cast<float*>(t), c.chunks, c.groups, set.rank_tiles, c.col_groups, false, kWaves};
+    // a wave has the loads of 8 steps on their way at once
+    const int64_t steps = set.k_pad >> 5;
+    a.share = steps <= 8 ? 1 : (steps <= 16 ? 2 : (steps <= 32 ? 4 : kWaves));
     a.quads = set.N % 4 == 0 && ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
     return a;
 }
@@ -663,9 +679,8 @@ hipError_t launch_adapters_add(const AdapterSet& set, const void* x, int x_dtype
     const Cut c = cut_of(set, M);
     const AdapterArgs a = args_of(set, c, x, M, slot, y, out, ws);
     const dim3 up((unsigned)(c.tiles * c.col_groups));
-    // One launch where every workgroup can compute t in about the time of a launch: up to 256 KB of factors (us with the
-    // linear, K = N = 2048, rank 16, bf16: 1 row 10.7 against 13.9 in two launches, 4 rows 14.1 and 15.2, 8 rows, 512 KB,
-    // 17.9 and 16.6).
+    // One launch where every workgroup can compute t in about the time of a launch: up to 256 KB of factors (us, K = N = 2048,
+    // rank 16, bf16: 1 row 6.4, 2 rows 8.2, 4 rows 10.1, 256 KB; in two launches 10.3).
     const int64_t again = M * set.rank_tiles * 32 * set.k_pad;
     if (M <= 16 && set.rank_tiles <= 2 && octets(set, x, x_dtype) && again <= (256 << 10)) {
 #define Q4GSW_ONE(FT) \
