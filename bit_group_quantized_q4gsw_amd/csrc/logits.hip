@@ -26,6 +26,8 @@ constexpr int kThreads = 256, kOwnLoads = kTreeMax / kThreads, kLoads = 8, kItem
 // Of a token's count: among the prompt's; listed; one of the rows' tokens.
 constexpr uint32_t kPrompt = 0x80000000u, kListed = 0x40000000u, kOwn = 0x20000000u;
 
+__host__ __device__ constexpr int in_quads(int n) { return (n + 3) & ~3; }
+
 // Four neighbouring logits as they lie in memory.
 template <int DT>
 struct Quad {
@@ -142,8 +144,8 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a) {
     uint32_t* const s_bias = lds + C;                         // [C], where biases are given: entry + 1
     uint32_t* const s_listed = lds + (a.bias_ids ? 2 * C : C);
     uint16_t* const s_list = reinterpret_cast<uint16_t*>(s_listed + 4);                       // [C]
-    int32_t* const s_ids = reinterpret_cast<int32_t*>(s_list + C);                            // [max_new], where given
-    const KvTree tree(reinterpret_cast<uint8_t*>(s_ids + (a.ids ? a.max_new : 0)), a.max_new);
+    int32_t* const s_ids = reinterpret_cast<int32_t*>(s_list + C);                            // [max_new in quads], where given
+    const KvTree tree(reinterpret_cast<uint8_t*>(s_ids + (a.ids ? in_quads(a.max_new) : 0)), a.max_new);
 
     auto here = [&](int64_t id) -> bool { return id >= v0 && id < v0 + C && id < a.V; };
     // a token's first mark lists it
@@ -276,8 +278,13 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a) {
                     if (c & kOwn) {
                         const int node = (int)(l - first);
                         const uint32_t* bits = tree.bits + r[k] * tree.stride + 1;
-                        for (int j = 0; j <= node; ++j)
-                            if (s_ids[j] == v && (!a.parents || ((bits[j >> 5] >> (j & 31)) & 1u))) ++c;
+                        for (int j = 0; j <= node; j += 4) {
+                            const u4 id = *reinterpret_cast<const u4*>(s_ids + j);
+                            uint32_t on = a.parents ? bits[j >> 5] >> (j & 31) : ~0u;
+                            if (node - j < 3) on &= (2u << (node - j)) - 1u;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) c += (on >> e) & (id[e] == (uint32_t)v ? 1u : 0u);
+                        }
                     }
                     c &= ~(kListed | kOwn);
                     float z = y[k];
@@ -302,7 +309,7 @@ int quads_of(const LogitsArgs& a) { return a.rows * chunks_of(a.V, kWide) >= 512
 int lds_bytes(const LogitsArgs& a, int quads, int rows) {
     const int C = 4 * quads * kThreads;
     if (!a.history && !a.ids && !a.bias_ids) return 0;
-    return 4 * C + (a.bias_ids ? 4 * C : 0) + 16 + 2 * C + (a.ids ? 4 * a.max_new : 0) + (a.parents ? tree_bytes(a.max_new, rows) : 0);
+    return 4 * C + (a.bias_ids ? 4 * C : 0) + 16 + 2 * C + (a.ids ? 4 * in_quads(a.max_new) : 0) + (a.parents ? tree_bytes(a.max_new, rows) : 0);
 }
 
 // Rows of one sequence share the count of its history: as many to a workgroup as let all workgroups run at once.
