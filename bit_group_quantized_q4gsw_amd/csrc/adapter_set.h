@@ -38,7 +38,6 @@ struct AdapterArgs {
     int groups;              // workgroups that share a tile's adapters in the first launch
     int rank_tiles;
     int64_t col_groups;
-    bool quads;              // rows of y and out hold aligned quads
     int share;               // waves that share a chunk of K
 };
 

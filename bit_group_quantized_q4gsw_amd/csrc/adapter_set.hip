@@ -33,6 +33,8 @@
 namespace q4gsw {
 namespace {
 
+// rows of y and out in memory, at the alignment of an element, which vector loads and stores take
+typedef float f4_at4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 
@@ -298,8 +300,8 @@ __global__ __launch_bounds__(KIND == kOne ? 64 * kWaves : 256) void up_kernel(Ad
             acc[j][h] = base[j][h] = f4{0.f, 0.f, 0.f, 0.f};
             const int64_t n = col(j, h);
             if (here) {
-                if (a.quads) {
-                    if (n < a.N) base[j][h] = *reinterpret_cast<const f4*>(a.y + m * a.N + n);
+                if (n + 4 <= a.N) {
+                    base[j][h] = *reinterpret_cast<const f4_at4*>(a.y + m * a.N + n);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -405,8 +407,8 @@ __global__ __launch_bounds__(KIND == kOne ? 64 * kWaves : 256) void up_kernel(Ad
             f4 v = base[j][h];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = FT == kF16 ? fmaf(acc[j][h][e], inv, v[e]) : v[e] + acc[j][h][e];
-            if (a.quads) {
-                if (n < a.N) *reinterpret_cast<f4*>(a.out + m * a.N + n) = v;
+            if (n + 4 <= a.N) {
+                *reinterpret_cast<f4_at4*>(a.out + m * a.N + n) = v;
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -503,8 +505,8 @@ __global__ __launch_bounds__(256) void join_kernel(AdapterArgs a, const float* _
     const int64_t mo = 32 * tm + row, n = 32 * tn + c4;
     if (mo >= a.M) return;
     float* dst = a.out + mo * a.N + n;
-    if (a.quads) {
-        if (n < a.N) *reinterpret_cast<f4*>(dst) = f4{s_tile[row][c4], s_tile[row][c4 + 1], s_tile[row][c4 + 2], s_tile[row][c4 + 3]};
+    if (n + 4 <= a.N) {
+        *reinterpret_cast<f4_at4*>(dst) = f4_at4{s_tile[row][c4], s_tile[row][c4 + 1], s_tile[row][c4 + 2], s_tile[row][c4 + 3]};
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -632,11 +634,10 @@ namespace {
 
 AdapterArgs args_of(const AdapterSet& set, const Cut& c, const void* x, int64_t M, const int32_t* slot, const float* y, float* out,
                     void* t) {
-    AdapterArgs a{set, x, M, set.K, set.N, slot, y, out, static_cast<float*>(t), c.chunks, c.groups, set.rank_tiles, c.col_groups, false, kWaves};
+    AdapterArgs a{set, x, M, set.K, set.N, slot, y, out, static_cast<float*>(t), c.chunks, c.groups, set.rank_tiles, c.col_groups, kWaves};
     // a wave has the loads of 8 steps on their way at once
     const int64_t steps = set.k_pad >> 5;
     a.share = steps <= 8 ? 1 : (steps <= 16 ? 2 : (steps <= 32 ? 4 : kWaves));
-    a.quads = set.N % 4 == 0 && ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
     return a;
 }
 

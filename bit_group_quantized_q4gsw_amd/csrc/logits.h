@@ -25,7 +25,6 @@ struct LogitsArgs {
     const uint32_t* mask;                // null: none
     int64_t mask_ld;
     int chunks, rows_per_group;
-    bool quads;                          // rows hold aligned quads
 };
 
 hipError_t launch_logits(LogitsArgs a, int dtype, hipStream_t s);

@@ -28,17 +28,21 @@ constexpr uint32_t kPrompt = 0x80000000u, kListed = 0x40000000u, kOwn = 0x200000
 
 __host__ __device__ constexpr int in_quads(int n) { return (n + 3) & ~3; }
 
+// Vectors in memory at the alignment of an element, which vector loads and stores take.
+typedef uint32_t u4_at4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u2_at2 __attribute__((ext_vector_type(2), aligned(2)));
+
 // Four neighbouring logits as they lie in memory.
 template <int DT>
 struct Quad {
     uint32_t w[DT == kF32 ? 4 : 2];
     __device__ __forceinline__ void load(const void* p, int64_t at) {
         if constexpr (DT == kF32) {
-            const u4 v = ldg16(static_cast<const float*>(p) + at);
+            const u4_at4 v = *reinterpret_cast<const u4_at4*>(static_cast<const float*>(p) + at);
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = v[e];
         } else {
-            const u2 v = *reinterpret_cast<const u2*>(static_cast<const uint16_t*>(p) + at);
+            const u2_at2 v = *reinterpret_cast<const u2_at2*>(static_cast<const uint16_t*>(p) + at);
             w[0] = v[0];
             w[1] = v[1];
         }
@@ -59,10 +63,10 @@ struct Quad {
         }
     }
     __device__ __forceinline__ void store(void* p, int64_t at) const {
-        if constexpr (DT == kF32) *reinterpret_cast<u4*>(static_cast<float*>(p) + at) = u4{w[0], w[1], w[2], w[3]};
-        else *reinterpret_cast<u2*>(static_cast<uint16_t*>(p) + at) = u2{w[0], w[1]};
+        if constexpr (DT == kF32) *reinterpret_cast<u4_at4*>(static_cast<float*>(p) + at) = u4_at4{w[0], w[1], w[2], w[3]};
+        else *reinterpret_cast<u2_at2*>(static_cast<uint16_t*>(p) + at) = u2_at2{w[0], w[1]};
     }
-    // one by one, `n` of them (rows that hold no aligned quads)
+    // one by one, `n` of them (a row's last)
     __device__ __forceinline__ void load(const void* p, int64_t at, int64_t n) {
         for (uint32_t& v : w) v = 0u;
 #pragma unroll
@@ -173,7 +177,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a) {
                 for (int k = 0; k < Q; ++k) {
                     const int64_t v = v0 + 4 * (tid + k * kThreads), l = row + r;         // its quad's mask is in one word
                     if (v >= a.V) continue;
-                    if (a.quads) x[r][k].load(a.logits, l * a.ld + v);
+                    if (v + 4 <= a.V) x[r][k].load(a.logits, l * a.ld + v);
                     else x[r][k].load(a.logits, l * a.ld + v, a.V - v);
                     if (a.mask) allowed[r][k] = a.mask[l * a.mask_ld + (v >> 5)];
                 }
@@ -246,7 +250,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a) {
                     const int64_t v = v0 + 4 * (tid + k * kThreads), l = row + r;
                     if (v >= a.V) continue;
                     if (a.mask) x[r][k].mask(allowed[r][k] >> (v & 31));
-                    if (a.quads) x[r][k].store(a.out, l * a.out_ld + v);
+                    if (v + 4 <= a.V) x[r][k].store(a.out, l * a.out_ld + v);
                     else x[r][k].store(a.out, l * a.out_ld + v, a.V - v);
                 }
             }
@@ -339,8 +343,6 @@ hipError_t launch_logits(LogitsArgs a, int dtype, hipStream_t s) {
     const int quads = quads_of(a);
     a.chunks = chunks_of(a.V, quads);
     a.rows_per_group = group_rows(a, quads, a.chunks);
-    const uintptr_t at = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.out);
-    a.quads = a.V % 4 == 0 && a.ld % 4 == 0 && a.out_ld % 4 == 0 && (at & (dtype == kF32 ? 15u : 7u)) == 0;
 #define Q4GSW_LOGITS(DT) return quads == 1 ? launch<DT, 1>(a, s) : launch<DT, kWide>(a, s)
     switch (dtype) {
         case kF32: Q4GSW_LOGITS(kF32);

@@ -518,7 +518,7 @@ q4gsw_status q4gsw_logits_adjust(const void* logits, int32_t dtype, int64_t rows
     if (!logits || !out) return Q4GSW_E_NULL;
     LogitsArgs a{logits, out, rows, vocab, ld, out_ld, r->batch, r->max_new, r->cu, r->history, r->history_ld, r->history_cols,
                  r->history_len, r->prompt_len, r->ids, r->parents, r->repetition, r->presence, r->frequency, r->bias_ids,
-                 r->bias, r->bias_ld, r->bias_cols, r->mask, r->mask_ld, 0, 0, false};
+                 r->bias, r->bias_ld, r->bias_cols, r->mask, r->mask_ld, 0, 0};
     if (!r->history) a.prompt_len = nullptr;
     if (!r->cu) a.max_new = 1;
     if (!logits_launch_ok(a)) return Q4GSW_E_SHAPE;
