@@ -145,7 +145,9 @@ AttnPlan plan_rows(const AttnSize& n) {
 // nodes (256): 39 (47), 42 (51), 46 (56), 51 (65); 64 nodes (1024): 88 (117), 98 (128).  In tiles of 16, 8 sequences of
 // 26 nodes, window 1024, 16 / 4 heads of 256 (224 workgroups): 1 split 24, 2 splits 32; up to 32 blocks none pay: 521
 // tokens, heads of 64: 1 split 9.2, 2 splits 13.7.
-AttnPlan plan_tiles(const AttnSize& n, int tile, int most, float unit, float start) {
+// `waves`: what a SIMD holds; `start`: us of a workgroup's first loads, tree and join, which the next turn of workgroups pays
+// again (43 sequences of 62 nodes and 103 tokens, 24 / 4 heads of 192, fp16, 4128 tiles of 16 rows: 78, estimate 73).
+AttnPlan plan_tiles(const AttnSize& n, int tile, int most, int waves, float unit, float start) {
     AttnPlan p{};
     p.row_tiles = (n.rows + tile - 1) / tile;
     const int64_t groups = (int64_t)n.batch * n.heads * p.row_tiles, blocks = n.blocks(tile);
@@ -153,14 +155,17 @@ AttnPlan plan_tiles(const AttnSize& n, int tile, int most, float unit, float sta
     if (blocks > 32) splits = kCus / groups < blocks / 8 ? kCus / groups : blocks / 8;
     finish_plan(p, n, blocks, splits);
     p.waves = groups * p.splits <= kCus ? most : 4;
-    const float all = groups * n.mean / kCus, longest = (float)((p.chunk + p.waves - 1) / p.waves * p.waves);
-    p.us += start + unit * (longest > all ? longest : all);
+    const int64_t all = groups * p.splits;
+    const float turns = (float)all * p.waves / (kCus * 4 * waves);
+    const float per_cu = turns <= 1 ? (float)((all + kCus - 1) / kCus) : (float)all / kCus;
+    const float longest = (float)((p.chunk + p.waves - 1) / p.waves * p.waves), mean = per_cu * n.mean / p.splits;
+    p.us += start * (turns < 1 ? 1 : turns) + unit * (longest > mean ? longest : mean);
     return p;
 }
 
 AttnPlan plan_tree(const AttnSize& n) {
     const float unit = n.dim <= 192 ? 0.04f + 0.0017f * n.dim : 0.6f;       // one wave a SIMD at 256 channels
-    AttnPlan p = plan_tiles(n, 32, kv_tree_most(n.dim), unit * (n.prec ? 1.25f : 1.0f), 4.5f + 0.035f * n.dim);
+    AttnPlan p = plan_tiles(n, 32, kv_tree_most(n.dim), kv_tree_waves(n.dim, n.prec), unit * (n.prec ? 1.25f : 1.0f), 4.5f + 0.035f * n.dim);
     p.kernel = AttnPlan::kTree;
     return p;
 }
@@ -232,8 +237,9 @@ AttnSize attention_size(int heads, int dim, int batch, int hq, int max_new, int 
 AttnPlan plan_attention(const AttnSize& n, int kernel) {
     if (kernel == Q4GSW_KV_MANY_ROWS) return plan_prompt(n);
     if (kernel == Q4GSW_KV_TREE) return plan_tree(n);
-    AttnPlan few = n.tree ? plan_tiles(n, 16, 8, 0.06f + 0.00105f * n.dim, 4.0f + 0.02f * n.dim) : plan_rows(n);
+    AttnPlan few = n.tree ? plan_tiles(n, 16, 8, kv_rows_waves(n.dim), 0.06f + 0.00105f * n.dim, 4.0f + 0.02f * n.dim) : plan_rows(n);
     if (kernel == Q4GSW_KV_FEW_ROWS) return few;
+    // (of 140 drawn calls of 10 to 120 us the estimates take a kernel slower by over 10% for 6, by 42% at most)
     // a tree's tiles of 32 rows cost less VALU a row, tiles of 16 spread over more CUs and start sooner (us of 16 nodes of
     // 600 tokens, 32 / 8 heads of 128, bf16: 10.5 against 14.2; the batch of plan_tiles' comment, 8 nodes: 31 against 27, 32
     // nodes in fp16 77 and 81)
