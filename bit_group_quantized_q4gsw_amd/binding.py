@@ -991,7 +991,7 @@ def adapters_add(y: torch.Tensor, x: torch.Tensor, s: Adapters, slots: torch.Ten
                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """out [M, N] fp32: y[m] (fp32; a projection of the same rows) + alpha_i (x[m] A_i^T) B_i^T for the adapter in
     slot i = slots[m].  `out` may be y itself."""
-    done = _host.adapters(0, s._addr, s._dev, x, slots, y, out, workspace)
+    done = _host.adapters(None, s._addr, s._dev, x, slots, y, out, workspace)
     if done is not None:
         return _done(done, "q4gsw_adapters_add")
     x, code, slots, M = _adapter_rows(x, s, slots)

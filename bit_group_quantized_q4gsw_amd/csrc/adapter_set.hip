@@ -18,8 +18,8 @@
 // is read from L2 by all but the first.
 //
 // Bound: bytes of the factors and latency: 61 rows of 48 adapters, rank 32, K = 8192, N = 2048, fp32 rows, fp16 factors:
-// 12 us (29 MB through L2, 18 from HBM) + 5 us; 64 rows of 32 adapters, rank 16, K = 2048, N = 8192: 6.4 + 7 us.  Prompts: the
-// second launch's y, read and written: 2048 rows of 8192: 7.5 + 33 us for 134 MB.
+// 11.4 us (29 MB through L2, 18 from HBM) + 4.7 us; 64 rows of 32 adapters, rank 16, K = 2048, N = 8192: 5.4 us and the sum.  Prompts:
+// the second launch's y, read and written: 2048 rows of 8192: 7.4 + 30 us for 134 MB.
 //
 // Numbers: products of 16-bit factors are exact in the matrix unit's fp32, so what rows and t lose on
 // their way into 16-bit operands is all that is lost.  They enter as sums of parts: with bf16 factors one

@@ -279,10 +279,10 @@ PyObject* keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// (weight or 0, set, device, x, slots, y or None, out or None, workspace or None): out
+// (weight or None, set, device, x, slots, y or None, out or None, workspace or None): out
 PyObject* adapters(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return regular(n, 8, [&]() -> PyObject* {
-        const q4gsw_weight* w = static_cast<const q4gsw_weight*>(PyLong_AsVoidPtr(a[0]));
+        const q4gsw_weight* w = a[0] == Py_None ? nullptr : address<const q4gsw_weight>(a[0]);
         const q4gsw_adapters* set = address<const q4gsw_adapters>(a[1]);
         const int dev = int32(a[2]);
         const at::Tensor& x = tensor(a[3], dev);

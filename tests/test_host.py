@@ -23,12 +23,14 @@ def test_calls_that_are_not_regular_are_left_to_python():
         assert h.append(a, dev, x, x, *where) is None
         assert h.read(a, dev, *where, 3) is None
         assert h.keep([a], dev, i, i[:1], *where, 3, None, None) is None
-        assert h.adapters(0, a, dev, x[:, 0], i, x[:, 0], None, None) is None
+        assert h.adapters(None, a, dev, x[:, 0], i, x[:, 0], None, None) is None
     for bad in (None, 3, "x", [None], 1.5):
         assert h.logits(bad, *[None] * 14) is None
         assert h.append(a, 0, bad, bad, *where) is None
         assert h.append(bad if bad != 3 else None, 0, x, x, *where) is None
         assert h.keep(bad, 0, i, i[:1], *where, 3, None, None) is None
+        if bad is not None:
+            assert h.adapters(bad if bad != 3 else "3", a, 0, x, i, x, None, None) is None
         assert h.attention(a, 1 << 40, bad, None, *where, bad, 3, 0, 0.0, None, None) is None
     assert h.logits(torch.zeros(2, 5), None, 1, *[None] * 12) is None
     assert h.logits(torch.zeros(2, 5, device="meta"), None, 1, *[None] * 12) is None
