@@ -343,7 +343,7 @@ __global__ __launch_bounds__(KIND == kOne ? 64 * kWaves : 256) void up_kernel(Ad
         uint32_t left = first_rows(mine, i);
         int order = mine >= 0 ? __popc(left & ((1u << first) - 1u)) : -1;     // of the row's adapter
         for (; left; order -= ways) {
-            uint32_t one = 0u;                                // the wave's adapter of this round
+            uint32_t one = 0u;                                // the wave's adapter of this turn
             for (int w = 0; w < ways; ++w) {
                 const uint32_t low = left & (0u - left);
                 one = w == way ? low : one;

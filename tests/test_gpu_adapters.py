@@ -295,3 +295,29 @@ def test_in_the_sum_of_a_split_linear(m, n, k, rank, slots, xtype, ftype):
     got = q.adapters_fwd(w, x.cuda(), s, ints(at))
     keep = torch.arange(m) != m // 2
     assert torch.equal(got.cpu()[keep], q.adapters_add(y, x.cuda(), s, ints(at)).cpu()[keep])
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 256, 512), (5, 100, 96), (40, 2052, 2048), (40, 333, 1024), (1100, 260, 64)])
+def test_rows_that_are_not_aligned(m, n, k):
+    """y and out one element past an aligned address: the same values, and nothing beside them."""
+    q = lib()
+    g = torch.Generator().manual_seed(n)
+    ad = factors(4, 8, n, k, F16, seed=2)
+    s = make(q, ad, 8, n, k, F16)
+    w = q.pack(torch.randint(0, 16, (n, k), generator=g, dtype=torch.uint8).cuda(),
+               (0.01 + 0.01 * torch.rand(k // 32, n, generator=g)).half().cuda(), 32)
+    x, y, at = torch.randn(m, k, generator=g).to(BF16).cuda(), torch.randn(m, n, generator=g).cuda(), ints(some_slots(m, 4, 1))
+
+    def moved(t):
+        return torch.cat([t.new_full((1,), 3.0), t.flatten()])[1:].view(t.shape)
+
+    def room():
+        return torch.full((m * n + 1 + 8,), 9.0, device="cuda")
+    out = room()
+    got = q.adapters_add(moved(y), x, s, at, out=out[1:1 + m * n].view(m, n))
+    assert torch.equal(got, q.adapters_add(y, x, s, at))
+    assert (out[:1] == 9).all() and (out[1 + m * n:] == 9).all()           # nothing beside the rows
+    out = room()
+    got = q.adapters_fwd(w, x, s, at, out=out[1:1 + m * n].view(m, n))
+    assert torch.equal(got, q.adapters_fwd(w, x, s, at))
+    assert (out[:1] == 9).all() and (out[1 + m * n:] == 9).all()

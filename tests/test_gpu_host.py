@@ -160,3 +160,88 @@ def test_refusals_are_the_librarys_and_pythons():
         q.logits_adjust(x, parents=torch.zeros(12, dtype=I32, device="cuda"))
     with pytest.raises(q.Q4gswError):
         q.logits_adjust(x[:, :300], out=x[:, 20:320])                                                  # out over the logits, shifted
+
+
+def step(q, s, a, x, y, at, logits, more):
+    """One step's calls on the current stream; nothing is written that another step reads."""
+    where = (s["table"], s["cu"], s["lens"])
+    return [q.kv_tree_attention(s["caches"][0], s["q"], s["parents"], *where, 7, 130), q.adapters_add(y, x, a, at),
+            q.logits_adjust(logits, **more)]
+
+
+def steps(q, seed):
+    g = torch.Generator().manual_seed(seed)
+    n, k, m = 320, 512, 40
+    a = q.adapters(6, 16, n, k)
+    for i in range(6):
+        q.adapters_load(a, i, torch.randn(16, k, generator=g).cuda(), torch.randn(n, 16, generator=g).cuda(), 0.5)
+    return (q, state(q), a, torch.randn(m, k, generator=g).cuda(), torch.randn(m, n, generator=g).cuda(),
+            torch.randint(-1, 6, (m,), generator=g, dtype=I32).cuda(), torch.randn(12, 333, generator=g).cuda(), rules())
+
+
+def test_two_streams_at_once():
+    q = lib()
+    both = [steps(q, i) for i in range(2)]
+    want = [step(*b) for b in both]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for b, stream, out in zip(both, streams, got):
+            with torch.cuda.stream(stream):
+                out.append(step(*b))
+    torch.cuda.synchronize()
+    for w, out in zip(want, got):
+        for one in out:
+            assert all(torch.equal(x, y) for x, y in zip(w, one))
+
+
+def test_two_threads_at_once():
+    import threading
+    q = lib()
+    both = [steps(q, i) for i in range(2)]
+    want = [step(*b) for b in both]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got[i].append(step(*both[i]))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:                                     # shown by the main thread
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for w, out in zip(want, got):
+        assert len(out) == 20
+        for one in out:
+            assert all(torch.equal(x, y) for x, y in zip(w, one))
+
+
+def test_captured_without_outputs():
+    """Outputs and workspaces that the calls allocate themselves live in the graph's memory."""
+    q = lib()
+    args = steps(q, 4)
+    want = step(*args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*args)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(*args)
+    for _ in range(3):
+        for x in got:
+            x.zero_()
+        junk = torch.randn(1 << 20, device="cuda")                 # eager work between the replays
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+        del junk
