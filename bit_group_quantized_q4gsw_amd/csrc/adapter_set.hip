@@ -584,7 +584,7 @@ hipError_t one_launch(const AdapterArgs& a, dim3 grid, hipStream_t s) {
 struct Cut {
     int64_t tiles;
     int chunks, groups;
-    bool many;
+    bool many, one;                      // the column groups are up_kernel's: kMany, else kFew and, if one launch may do, kOne
     int64_t col_groups;
 };
 Cut cut_of(const AdapterSet& set, int64_t M) {
@@ -594,6 +594,9 @@ Cut cut_of(const AdapterSet& set, int64_t M) {
     c.chunks = (int)(c.tiles >= 1024 || steps <= 64 ? 1 : (steps >= 64 * kMostChunks ? kMostChunks : (steps + 63) / 64));
     c.groups = M <= 256 ? (int)(M < 16 ? M : 16) : 2;
     c.many = c.tiles * ((set.N + 255) / 256) >= 1024;
+    // One launch where every workgroup can compute t in about the time of a launch: up to 256 KB of factors (us, K = N = 2048,
+    // rank 16, bf16: 1 row 6.4, 2 rows 8.2, 4 rows 10.1, 256 KB; in two launches 10.3).
+    c.one = !c.many && M <= 16 && set.rank_tiles <= 2 && M * set.rank_tiles * 32 * set.k_pad <= (256 << 10);
     const int cols = c.many ? 256 : (set.rank_tiles == 1 ? 64 : 32);
     c.col_groups = (set.N + cols - 1) / cols;
     return c;
@@ -603,7 +606,8 @@ Cut cut_of(const AdapterSet& set, int64_t M) {
 
 bool adapters_launch_ok(const AdapterSet& set, int64_t M) {
     const Cut c = cut_of(set, M);
-    const int64_t most = (int64_t(1) << 32) - 1;                 // threads of a grid
+    // threads of a grid; one launch for all, whose workgroups are twice as large, has fewer than 2^13 of them
+    const int64_t most = (int64_t(1) << 32) - 1;
     return c.tiles * c.groups * set.rank_tiles <= most / (64 * kWaves * c.chunks) && c.tiles <= most / 256 / c.col_groups;
 }
 
@@ -680,10 +684,7 @@ hipError_t launch_adapters_add(const AdapterSet& set, const void* x, int x_dtype
     const Cut c = cut_of(set, M);
     const AdapterArgs a = args_of(set, c, x, M, slot, y, out, ws);
     const dim3 up((unsigned)(c.tiles * c.col_groups));
-    // One launch where every workgroup can compute t in about the time of a launch: up to 256 KB of factors (us, K = N = 2048,
-    // rank 16, bf16: 1 row 6.4, 2 rows 8.2, 4 rows 10.1, 256 KB; in two launches 10.3).
-    const int64_t again = M * set.rank_tiles * 32 * set.k_pad;
-    if (M <= 16 && set.rank_tiles <= 2 && octets(set, x, x_dtype) && again <= (256 << 10)) {
+    if (c.one && octets(set, x, x_dtype)) {
 #define Q4GSW_ONE(FT) \
     (x_dtype == kF32 ? one_launch<FT, kF32>(a, up, s) : (x_dtype == kF16 ? one_launch<FT, kF16>(a, up, s) : one_launch<FT, kBF16>(a, up, s)))
         return set.dtype == kF16 ? Q4GSW_ONE(kF16) : Q4GSW_ONE(kBF16);

@@ -321,3 +321,34 @@ def test_rows_that_are_not_aligned(m, n, k):
     got = q.adapters_fwd(w, x, s, at, out=out[1:1 + m * n].view(m, n))
     assert torch.equal(got, q.adapters_fwd(w, x, s, at))
     assert (out[:1] == 9).all() and (out[1 + m * n:] == 9).all()
+
+
+def packed(q, n, k, g):
+    return q.pack(torch.randint(0, 16, (n, k), generator=g, dtype=torch.uint8).cuda(),
+                  (0.01 + 0.01 * torch.rand(k // 32, n, generator=g)).half().cuda(), 32)
+
+
+@pytest.mark.parametrize("rank", [16, 32])
+@pytest.mark.parametrize("m", [1, 4])
+@pytest.mark.parametrize("n", [261888, 261889, 262144, 262400])
+def test_few_rows_of_an_output_layer(n, m, rank):
+    """Outputs as wide as a vocabulary, on both sides of the change from narrow column groups to wide ones: every column of
+    an `out` that holds NaN before, in place, and beside the linear."""
+    q = lib()
+    k = 64
+    ad = factors(2, rank, n, k, BF16, seed=rank)
+    s = make(q, ad, rank, n, k, BF16)
+    g = torch.Generator().manual_seed(m)
+    x, y, at = torch.randn(m, k, generator=g).to(BF16), torch.randn(m, n, generator=g), [i % 2 for i in range(m)]
+    want, bound = formula(y, x, ad, at, BF16)
+    out = torch.full((m, n), float("nan"), device="cuda")
+    got = q.adapters_add(y.cuda(), x.cuda(), s, ints(at), out=out)
+    check(got, want, bound, f"wide add m={m} n={n} rank={rank}")
+    yd = y.cuda()
+    assert torch.equal(q.adapters_add(yd, x.cuda(), s, ints(at), out=yd), got)
+    w = packed(q, n, k, g)
+    base = q.linear_fwd(w, x.cuda())
+    out.fill_(float("nan"))
+    got = q.adapters_fwd(w, x.cuda(), s, ints(at), out=out)
+    want, bound = formula(base.cpu(), x, ad, at, BF16)
+    check(got, want, bound, f"wide fwd m={m} n={n} rank={rank}")
