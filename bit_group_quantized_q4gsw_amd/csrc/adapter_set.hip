@@ -195,7 +195,7 @@ __global__ __launch_bounds__(64 * kWaves) void down_kernel(AdapterArgs a) {
     const int mine = row_slot(a, tile, i);
     uint32_t firsts = first_rows(mine, i);
     const int64_t m = 16 * tile + i, row = m * a.K;
-    // the waves from a.share on have none of it, so that one launch for few rows sums in the same order
+    // the waves from a.share on have none of it, so that one launch for few rows, whose waves share K alike, sums in the same order
     const int64_t steps = a.set.k_pad >> 5, parts = a.chunks * a.share, per = (steps + parts - 1) / parts;
     const int64_t begin = wave < a.share ? per * (chunk * a.share + wave) : steps, s1 = min(begin + per, steps);
     for (int n = 0; firsts; firsts &= firsts - 1, ++n) {
@@ -591,12 +591,13 @@ Cut cut_of(const AdapterSet& set, int64_t M) {
     Cut c;
     c.tiles = (M + 15) / 16;
     const int64_t steps = set.k_pad / 32;
-    c.chunks = (int)(c.tiles >= 1024 || steps <= 64 ? 1 : (steps >= 64 * kMostChunks ? kMostChunks : (steps + 63) / 64));
-    c.groups = M <= 256 ? (int)(M < 16 ? M : 16) : 2;
     c.many = c.tiles * ((set.N + 255) / 256) >= 1024;
     // One launch where every workgroup can compute t in about the time of a launch: up to 256 KB of factors (us, K = N = 2048,
     // rank 16, bf16: 1 row 6.4, 2 rows 8.2, 4 rows 10.1, 256 KB; in two launches 10.3).
     c.one = !c.many && M <= 16 && set.rank_tiles <= 2 && M * set.rank_tiles * 32 * set.k_pad <= (256 << 10);
+    // rows of x that one launch cannot load, since they are not aligned, are summed in its order: one chunk
+    c.chunks = (int)(c.one || c.tiles >= 1024 || steps <= 64 ? 1 : (steps >= 64 * kMostChunks ? kMostChunks : (steps + 63) / 64));
+    c.groups = M <= 256 ? (int)(M < 16 ? M : 16) : 2;
     const int cols = c.many ? 256 : (set.rank_tiles == 1 ? 64 : 32);
     c.col_groups = (set.N + cols - 1) / cols;
     return c;

@@ -352,3 +352,21 @@ def test_few_rows_of_an_output_layer(n, m, rank):
     got = q.adapters_fwd(w, x.cuda(), s, ints(at), out=out)
     want, bound = formula(base.cpu(), x, ad, at, BF16)
     check(got, want, bound, f"wide fwd m={m} n={n} rank={rank}")
+
+
+@pytest.mark.parametrize("k", [2080, 4096, 8192])
+@pytest.mark.parametrize("xtype,ftype", [(BF16, BF16), (F32, F16), (F16, BF16)])
+def test_one_row_off_its_alignment(k, xtype, ftype):
+    """Sums are in an order that depends on the sizes alone: a row of x at any address gives the same bits, whichever launches
+    may load it."""
+    q = lib()
+    n, rank = 70, 16
+    ad = factors(2, rank, n, k, ftype, seed=k)
+    s = make(q, ad, rank, n, k, ftype)
+    g = torch.Generator().manual_seed(k)
+    x, y, at = torch.randn(1, k, generator=g).to(xtype), torch.randn(1, n, generator=g), [1]
+    want, bound = formula(y, x, ad, at, ftype)
+    first = q.adapters_add(y.cuda(), x.cuda(), s, ints(at))
+    check(first, want, bound, f"aligned {k} {xtype} {ftype}")
+    xo = torch.empty(k + 1, dtype=xtype, device="cuda")[1:].view(1, k).copy_(x)
+    assert torch.equal(q.adapters_add(y.cuda(), xo, s, ints(at)), first)
