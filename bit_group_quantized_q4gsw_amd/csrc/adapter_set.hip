@@ -592,14 +592,16 @@ Cut cut_of(const AdapterSet& set, int64_t M) {
     c.tiles = (M + 15) / 16;
     const int64_t steps = set.k_pad / 32;
     c.many = c.tiles * ((set.N + 255) / 256) >= 1024;
-    // One launch where every workgroup can compute t in about the time of a launch: up to 256 KB of factors (us, K = N = 2048,
-    // rank 16, bf16: 1 row 6.4, 2 rows 8.2, 4 rows 10.1, 256 KB; in two launches 10.3).
-    c.one = !c.many && M <= 16 && set.rank_tiles <= 2 && M * set.rank_tiles * 32 * set.k_pad <= (256 << 10);
+    const int cols = c.many ? 256 : (set.rank_tiles == 1 ? 64 : 32);
+    c.col_groups = (set.N + cols - 1) / cols;
+    // One launch, in which every workgroup computes t again, where that costs less than the other launch: up to 128 KB of factors, read
+    // by at most one workgroup a CU (us in one launch / two, bf16, rank 16: K = 2048 and N up to 16384, 1 row 5.8 / 7.7, 2 rows 7.7 / 8.0,
+    // 4 rows, 256 KB, 11.5 / 8.5; 16 rows of K = 256 8.8 / 10.0, of 512 11.7 / 10.0; 1 row of K = 8192 8.5 / 7.8; 1 row of K = 2048 and
+    // N = 20000, two workgroups on some CUs, 9.7 / 7.9, N = 131072 33 / 10).  So few groups of so few rows are never kMany's.
+    c.one = c.col_groups <= 256 && M <= 16 && set.rank_tiles <= 2 && M * set.rank_tiles * 32 * set.k_pad <= (128 << 10);
     // rows of x that one launch cannot load, since they are not aligned, are summed in its order: one chunk
     c.chunks = (int)(c.one || c.tiles >= 1024 || steps <= 64 ? 1 : (steps >= 64 * kMostChunks ? kMostChunks : (steps + 63) / 64));
     c.groups = M <= 256 ? (int)(M < 16 ? M : 16) : 2;
-    const int cols = c.many ? 256 : (set.rank_tiles == 1 ? 64 : 32);
-    c.col_groups = (set.N + cols - 1) / cols;
     return c;
 }
 
@@ -607,7 +609,7 @@ Cut cut_of(const AdapterSet& set, int64_t M) {
 
 bool adapters_launch_ok(const AdapterSet& set, int64_t M) {
     const Cut c = cut_of(set, M);
-    // threads of a grid; one launch for all, whose workgroups are twice as large, has fewer than 2^13 of them
+    // threads of a grid; one launch for all, whose workgroups are twice as large, has at most 256 of them
     const int64_t most = (int64_t(1) << 32) - 1;
     return c.tiles * c.groups * set.rank_tiles <= most / (64 * kWaves * c.chunks) && c.tiles <= most / 256 / c.col_groups;
 }

@@ -370,3 +370,20 @@ def test_one_row_off_its_alignment(k, xtype, ftype):
     check(first, want, bound, f"aligned {k} {xtype} {ftype}")
     xo = torch.empty(k + 1, dtype=xtype, device="cuda")[1:].view(1, k).copy_(x)
     assert torch.equal(q.adapters_add(y.cuda(), xo, s, ints(at)), first)
+
+
+@pytest.mark.parametrize("m,k,n,rank,slots,xtype,ftype", [
+    (1, 2048, 130, 32, 3, BF16, F16), (1, 4096, 16384, 16, 2, BF16, BF16), (1, 4096, 16385, 16, 2, F16, BF16),
+    (1, 4104, 65, 16, 2, F32, BF16), (2, 1024, 8192, 17, 3, F16, F16), (2, 1024, 8193, 17, 3, F32, BF16), (5, 384, 33, 20, 5, F32, F16),
+    (16, 128, 516, 20, 16, BF16, F16), (16, 120, 516, 17, 3, F16, BF16), (16, 256, 1, 9, 16, F32, F16), (16, 264, 40, 9, 16, BF16, BF16)])
+def test_one_launch_and_just_past_it(m, k, n, rank, slots, xtype, ftype):
+    """Few rows up to 128 KB of factors and 256 column groups, and past them; `out` holds NaN before."""
+    q = lib()
+    ad = factors(slots, rank, n, k, ftype, seed=k)
+    s = make(q, ad, rank, n, k, ftype)
+    g = torch.Generator().manual_seed(m)
+    x, y, at = torch.randn(m, k, generator=g).to(xtype), torch.randn(m, n, generator=g), some_slots(m, slots, n)
+    want, bound = formula(y, x, ad, at, ftype)
+    yd, out = y.cuda(), torch.full((m, n), float("nan"), device="cuda")
+    check(q.adapters_add(yd, x.cuda(), s, ints(at), out=out), want, bound, f"{m} x {k} -> {n} rank {rank}")
+    assert torch.equal(q.adapters_add(yd, x.cuda(), s, ints(at), out=yd), out)
