@@ -12,6 +12,7 @@ import ctypes
 import os
 import struct
 import threading
+import warnings
 from typing import Optional, Tuple
 
 import torch
@@ -130,6 +131,30 @@ _lib: Optional[ctypes.CDLL] = None
 _host = None            # the module _host: regular serving calls, marshalled in C++ (csrc/host.cpp)
 
 
+class _Python:
+    """In the place of _host where it cannot be loaded: no call is regular, and all are marshalled in Python."""
+
+    @staticmethod
+    def _left(*args):
+        return None
+
+    attention = append = read = keep = adapters = logits = _left
+
+
+def _load_host(h: ctypes.CDLL):
+    """The module _host, or its stand-in where it was not built or was built for another torch."""
+    try:
+        from . import _host as host
+        if host.torch_version != torch.__version__.split("+")[0]:
+            raise ImportError(f"_host was built for torch {host.torch_version}")
+        host.open(h._handle, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        return host
+    except (ImportError, AttributeError) as e:
+        warnings.warn(f"serving calls are marshalled in Python, which takes longer ({e}); build again with "
+                      "python bit_group_quantized_q4gsw_amd/build.py", RuntimeWarning, stacklevel=3)
+        return _Python()
+
+
 def lib() -> ctypes.CDLL:
     """The loaded library; raises if it has not been built (no fallback exists)."""
     global _lib, _host
@@ -205,9 +230,7 @@ def lib() -> ctypes.CDLL:
         h.q4gsw_layout_version.restype = ctypes.c_uint32
         h.q4gsw_build_info.argtypes = []
         h.q4gsw_build_info.restype = ctypes.c_char_p
-        from . import _host as host
-        host.open(h._handle, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
-        _lib, _host = h, host
+        _lib, _host = h, _load_host(h)
     return _lib
 
 

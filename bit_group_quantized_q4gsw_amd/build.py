@@ -4,7 +4,8 @@ Each csrc/*.hip file is compiled by hipcc in parallel and the objects are linked
 into bit_group_quantized_q4gsw_amd/libq4gsw.so.  Every compile passes
 -Xclang -target-feature -Xclang -packed-fp32-ops so no packed-fp32 VALU
 instruction is generated.  csrc/host.cpp, the marshalling of torch tensors for the serving
-calls, becomes the module _host (_host.so) beside it, by the host compiler.
+calls, becomes the module _host (_host.so) beside it, by the host compiler; where there is no torch or
+no host compiler it is left out, and the binding marshals those calls in Python.
 """
 import concurrent.futures
 import glob
@@ -43,9 +44,16 @@ def _compile(src: str, verbose: bool) -> str:
 
 
 def _host(verbose: bool) -> None:
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if spec is None or spec.origin is None or cxx is None:
+        if os.path.exists(HOST):                     # of another environment
+            os.remove(HOST)
+        print(f"{HOST} is left out: " + ("no host compiler" if cxx is None else "no torch"), file=sys.stderr, flush=True)
+        return
+    torch = os.path.dirname(spec.origin)
     tmp = HOST + ".tmp"
-    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
            "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "host.cpp"), "-o", tmp,
            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
@@ -64,13 +72,13 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
         host = ex.submit(_host, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        host.result()
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, "-shared", f"--offload-arch={ARCH}", "-o", tmp, *objs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True, capture_output=not verbose)
-    os.replace(tmp, LIB)
+        tmp = LIB + ".tmp"
+        cmd = [HIPCC, "-shared", f"--offload-arch={ARCH}", "-o", tmp, *objs]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True, capture_output=not verbose)
+        os.replace(tmp, LIB)
+        host.result()                                # the library is there whatever becomes of _host
     return LIB
 
 
