@@ -998,6 +998,8 @@ def adapters_fwd(w: PackedWeight, x: torch.Tensor, s: Adapters, slots: torch.Ten
                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [M, N] fp32: y[m] = x[m] . dequant(W)^T + alpha_i (x[m] A_i^T) B_i^T for the adapter in slot i = slots[m]
     (int32 [M]; outside the set's slots: none)."""
+    if w.buffer.get_device() != s._dev:
+        raise ValueError(f"w must be on {s.buffer.device}")
     done = _host.adapters(ctypes.addressof(w.desc), s._addr, s._dev, x, slots, None, out, workspace)
     if done is not None:
         return _done(done, "q4gsw_adapters_fwd")

@@ -148,3 +148,15 @@ def test_binding_refuses_tensors_of_the_wrong_kind(q):  # noqa: F811
         q.adapters(1 << 32, 16, 24, 40)
     with pytest.raises(ValueError):
         q.adapters(4, 16, 24, 40, device="cpu")
+
+
+def test_a_weight_on_another_device(q):  # noqa: F811
+    """adapters_fwd launches on the device of the set and x; a weight elsewhere is refused before that."""
+    class Elsewhere:
+        def get_device(self):
+            return 1
+
+    s = q.Adapters(desc(q, n=256, k=512), torch.empty(0, dtype=torch.uint8))
+    w = q.PackedWeight(fake_desc(q, 256, 512, 64, 1, flags=1), Elsewhere())
+    with pytest.raises(ValueError, match="w must be on"):
+        q.adapters_fwd(w, torch.zeros(3, 512), s, torch.zeros(3, dtype=torch.int32))
