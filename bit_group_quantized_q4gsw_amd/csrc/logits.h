@@ -4,6 +4,8 @@
 
 namespace q4gsw {
 
+constexpr int kLogitsHistory = 1 << 28;   // tokens of a history: their count and a path's fit 29 bits
+
 struct LogitsArgs {
     const void* logits;
     void* out;

@@ -515,7 +515,9 @@ q4gsw_status q4gsw_logits_adjust(const void* logits, int32_t dtype, int64_t rows
     if (!r->cu && r->batch != rows) return Q4GSW_E_SHAPE;
     if (r->max_new < 1 || r->max_new > (r->cu && r->ids ? kTreeMax : kMaxM)) return Q4GSW_E_SHAPE;
     if (r->parents && (!r->cu || !r->ids)) return Q4GSW_E_NULL;
-    if (r->history && (r->history_cols < 0 || r->history_ld < r->history_cols || r->history_ld > kMaxDim)) return Q4GSW_E_SHAPE;
+    if (r->history && (r->history_cols < 0 || r->history_cols > kLogitsHistory || r->history_ld < r->history_cols ||
+                       r->history_ld > kMaxDim))
+        return Q4GSW_E_SHAPE;
     if (r->history && !r->history_len) return Q4GSW_E_NULL;
     if (r->bias_ids && (r->bias_cols < 0 || r->bias_ld < r->bias_cols || r->bias_ld > kMaxDim)) return Q4GSW_E_SHAPE;
     if (r->bias_ids && !r->bias) return Q4GSW_E_NULL;

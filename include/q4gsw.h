@@ -618,7 +618,7 @@ q4gsw_status q4gsw_kv_keep(const q4gsw_kv_cache *caches, int32_t count, const q4
  * and one rounding to the logits' type.  A mask that leaves nothing gives a row of -inf.
  * Rows belong to sequences as in q4gsw_kv_seqs: cu[b] .. cu[b + 1] - 1 to sequence b, or row r to sequence r
  * (cu NULL, batch rows).  Rows of no sequence, and rows of a sequence past max_new, are not touched.
- *   history      device int32 [batch][history_ld >= history_cols], or NULL: the first history_len[b] (device
+ *   history      device int32 [batch][history_ld >= history_cols], or NULL (history_cols at most 2^28): the first history_len[b] (device
  *                int32 [batch]; at most history_cols) entries of row b are the tokens sequence b has behind it,
  *                of which the first prompt_len[b] (device int32 [batch]; NULL: none) are seen but not generated
  *   ids          device int32 [rows], or NULL: the tokens of the rows themselves.  A row has seen and

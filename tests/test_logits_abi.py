@@ -61,3 +61,15 @@ def test_binding_refuses_tensors_of_the_wrong_kind(q):  # noqa: F811
     for bad in (x, x[0], x.long()):
         with pytest.raises(ValueError):
             q.logits_adjust(bad)
+
+
+def test_histories_whose_counts_would_not_fit(q):  # noqa: F811
+    """A token is counted in 29 bits with its path's: histories of up to 2^28 tokens."""
+    def go(cols):
+        r = rules(q, batch=1, history=FAKE << 20, history_cols=cols, history_ld=1 << 30, bias_ids=None, bias=None)
+        # an output over the mask: what passes the sizes is refused for that, before any launch
+        return q.lib().q4gsw_logits_adjust(X, q.F32, 1, 1000, 1000, ctypes.byref(r), AT["mask"], 1000, None)
+
+    assert go(1 << 28) == E_ALIAS
+    for cols in ((1 << 28) + 1, 1 << 29, 1 << 30):
+        assert go(cols) == E_SHAPE, cols
