@@ -9,7 +9,8 @@
 //
 // Each thread climbs from one node: its ancestors come in falling order, so a word of bits is complete
 // when the next smaller one begins, and every word is written once.  A step is one dependent LDS read,
-// some 0.05 us; the climb runs while the first keys are on their way.
+// some 0.09 us; the climb runs while the first keys are on their way, but one of a deep tree is longer (1024 tokens, 8
+// heads of 64, bf16, nodes in a chain against a star: 16 nodes 10.5 and 9.4 us, 64 15 and 9.5, 512 57 and 10.4).
 #pragma once
 #include "kv4.h"
 

@@ -16,6 +16,8 @@
 // Bound: HBM for large vocabularies: masking alone runs at a copy's rate (110 rows of 128256 fp32 logits: 24 us,
 // 4.7 TB/s); counts of 4096 tokens a sequence, paths and biases make it 36 us, since all workgroups count at
 // the same time and memory waits.  Few rows are latency: 8 rows of 32000 over 600 tokens 5 us a call.
+// Long histories bound all: every workgroup reads its sequence's whole (8 rows of 32000 or of 128256 over 8192 tokens 11 us,
+// 32768 30, 131072 88; 112 rows of 128256 in trees: 54, 124 and 379).
 #include "logits.h"
 
 namespace q4gsw {
