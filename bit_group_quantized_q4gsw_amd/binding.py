@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import re
 import struct
 import threading
 import warnings
@@ -145,7 +146,7 @@ def _load_host(h: ctypes.CDLL):
     """The module _host, or its stand-in where it was not built or was built for another torch."""
     try:
         from . import _host as host
-        if host.torch_version != torch.__version__.split("+")[0]:
+        if host.torch_version != re.match(r"[0-9.]*[0-9]", torch.__version__).group():      # the headers' has no suffix
             raise ImportError(f"_host was built for torch {host.torch_version}")
         host.open(h._handle, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
         return host

@@ -89,3 +89,11 @@ def test_a_host_that_does_not_compile_is_told(tmp_path, monkeypatch):
     with pytest.raises(RuntimeError, match="host.cpp"):
         b.build()
     assert os.path.exists(b.LIB)
+
+
+def test_a_torch_between_releases(tmp_path):
+    """Whose __version__ says more than the version that its headers give."""
+    host = "import torch\ntorch_version = torch.__version__.split('+')[0]\ntorch.__version__ = torch_version + 'a0+git1'\ndef open(*a): pass\n"
+    call = "import warnings\nwarnings.simplefilter('error', RuntimeWarning)\nimport bit_group_quantized_q4gsw_amd as q\nprint(q.binding._host.__name__)"
+    res = subprocess.run([sys.executable, "-c", call], cwd=package(tmp_path, host), capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and res.stdout.strip().endswith("_host"), res.stdout + res.stderr
